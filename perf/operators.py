@@ -359,7 +359,7 @@ def _own(s):
         return hta.chunk_attention_paged(s["q"], s["k_cache"], s["v_cache"], s["table"], s["prefix_len"],
                                          s["q_start"], window=case["window"], workspace=s["ws"], **cache)
     if "ws" not in s:
-        s["ws"] = hta.new_workspace(hta.Dims(case["B"], case["Hq"], case["Hkv"], case["D"], case["T"], s["L_cap"], 0.0))
+        s["ws"] = hta.new_q8_workspace(hta.Dims(case["B"], case["Hq"], case["Hkv"], case["D"], case["T"], s["L_cap"], 0.0))
     return hta.verify_paged(s["q"], s["k_cache"], s["v_cache"], s["table"], s["prefix_len"], s["k_tree"],
                             s["v_tree"], s["parent"], workspace=s["ws"], **cache)
 
