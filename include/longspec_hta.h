@@ -87,7 +87,8 @@ typedef enum {
     LONGSPEC_HTA_ERR_PIPELINE_TIMEOUT = -18,   /* a bounded in-kernel wait ran out */
     LONGSPEC_HTA_ERR_INTERNAL = -19,           /* a kernel precondition failed (a library bug) */
     LONGSPEC_HTA_ERR_BAD_BLOCK = -20,          /* a block_table entry outside [0, num_blocks) */
-    LONGSPEC_HTA_ERR_BAD_PATH = -21            /* accept_len outside [0, T] or a path entry outside [0, T) */
+    LONGSPEC_HTA_ERR_BAD_PATH = -21,           /* accept_len outside [0, T] or a path entry outside [0, T) */
+    LONGSPEC_HTA_ERR_BAD_RANGES = -22          /* q_start not ascending inside [0, N] */
 } longspec_hta_status;
 
 /* Problem sizes of one call.  scale 0 means 1/sqrt(D); otherwise > 0. */
@@ -420,6 +421,143 @@ LONGSPEC_HTA_API int longspec_hta_commit(const longspec_hta_dims *dims, void *k_
                                 const int32_t *accept_len, const int32_t *path, void *workspace,
                                 size_t workspace_bytes, cudaStream_t stream);
 LONGSPEC_HTA_API int longspec_hta_commit_paged(const longspec_hta_dims *dims, const longspec_hta_paged_kv *kv,
+                                int32_t *prefix_len, const void *k_tree, const void *v_tree,
+                                const int32_t *accept_len, const int32_t *path, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * New tokens on their way into attention: norm and rotation of the query
+ * and key heads, the append of K/V rows to a paged cache, attention of
+ * chunks of new tokens over that cache, and the cache held in 8 bits.
+ *
+ * longspec_hta_cache: a paged cache as in longspec_hta_paged_kv, in bf16
+ * (k_scale and v_scale null) or in e4m3 (both set, uint8
+ * [num_blocks][Hkv][block_size]; k_cache and v_cache then hold e4m3 codes in
+ * the same layout, 16-byte aligned).  A row x of D values is kept as D codes
+ * c and one byte e:
+ *   x ~ c * 2^(e - 127), 2^(e - 127) the smallest power of two with
+ *   max|x| <= 448 * 2^(e - 127), e clamped to [16, 134]
+ * (codes rounded to nearest even, saturated where e was clamped at 134).  A
+ * row with an infinity or a NaN is kept as e = 255 and reads back as NaN.
+ * The block table names the blocks of sequence b in key order as in
+ * longspec_hta_paged_kv. */
+typedef struct {
+    void *k_cache;
+    void *v_cache;
+    const int32_t *block_table;
+    int num_blocks;
+    int block_size;
+    int max_blocks;
+    uint8_t *k_scale;
+    uint8_t *v_scale;
+} longspec_hta_cache;
+
+/* Rows of heads, bf16: the D values of (b, token t, head h) start at element
+ * b * stride_b + t * stride_t + h * stride_h of p (device, 16-byte aligned;
+ * the strides multiples of 8).  Slices of a projection's output are passed
+ * as they are. */
+typedef struct {
+    void *p;
+    int64_t stride_b, stride_t, stride_h;
+} longspec_hta_heads;
+
+/* Norm and rotation of a query or key row x of D values at position pos:
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (q_weight / k_weight bf16 [D];
+ *                                               null: y = x)
+ *   for i < rot_dim/2: the pair (y[i], y[i + rot_dim/2]), interleaved: the
+ *   pair (y[2i], y[2i+1]), turned by pos * inv_freq[i] and multiplied by
+ *   scale: (a, b) -> scale * (a cos - b sin, b cos + a sin).
+ * Values from rot_dim on are not turned.  Computed in fp32 (the angle in
+ * fp64), rounded once to bf16.  Frequencies scaled for long contexts are the
+ * caller's inv_freq, the attention factor that goes with them is `scale`
+ * (> 0; 0 means 1). */
+typedef struct {
+    const float *inv_freq;      /* [rot_dim / 2], device */
+    int rot_dim;                /* even, 2..D */
+    int interleaved;
+    float scale;
+    const void *q_weight;
+    const void *k_weight;
+    float eps;                  /* >= 0 */
+} longspec_hta_rope;
+
+/* Norm and rotation of the heads of B*T tokens: q (Hq heads), k (Hkv heads),
+ * positions int32 [B][T], results into q_out and k_out, which may be q and k
+ * themselves (same pointer and strides) but must not overlap them otherwise.
+ * One kernel on `stream`.  Errors: NULL_POINTER, MISALIGNED (rows and weights
+ * 16 bytes, strides 8 elements, inv_freq and positions 4 bytes),
+ * INVALID_DIMS, UNSUPPORTED_D, INVALID_OPTION (the rope's fields). */
+LONGSPEC_HTA_API int longspec_hta_qk_norm_rope(int B, int T, int Hq, int Hkv, int D,
+                                const longspec_hta_heads *q, const longspec_hta_heads *k,
+                                const int32_t *positions, const longspec_hta_rope *rope,
+                                const longspec_hta_heads *q_out, const longspec_hta_heads *k_out,
+                                cudaStream_t stream);
+
+/* Append of new tokens' K/V rows to a paged cache.  The N tokens of the call
+ * are the chunks of B sequences one after the other: those of sequence b are
+ * q_start[b] .. q_start[b+1] - 1 (q_start int32 [B+1], device, ascending;
+ * chunks may be empty), token q_start[b] + t going to position
+ * prefix_len[b] + t.  prefix_len is not advanced.  k and v are rows of Hkv
+ * heads of N tokens (stride_b is not used).
+ * rope non-null: k is normed and rotated on its way (by its position), and
+ * so is q (Hq heads), whose rows go to q_out; the cache then holds rotated
+ * keys.  rope null: q and q_out are not used.
+ *   dims: B, Hq, Hkv, D, L_cap (the longest sequence the table maps), T = N;
+ *         T has no upper limit but rows and keys below 2^31; scale unused.
+ *   workspace: at least 256 bytes (the status word).
+ * Tokens from q_start[B] on are padding: nothing is read or written for them.
+ * N = 0 launches nothing.  Errors as the calls above; device-detected:
+ * BAD_RANGES (q_start not ascending inside [0, N]; rows of ranges out of
+ * order may or may not be written), PREFIX_LEN_RANGE (prefix_len[b] < 0 or
+ * prefix_len[b] + chunk > L_cap) and BAD_BLOCK: such a sequence's (token's)
+ * rows are not written, its q_out rows are NaN. */
+LONGSPEC_HTA_API int longspec_hta_append_paged(const longspec_hta_dims *dims, const longspec_hta_heads *q,
+                                const longspec_hta_heads *k, const longspec_hta_heads *v,
+                                const longspec_hta_rope *rope, const longspec_hta_cache *cache,
+                                const int32_t *prefix_len, const int32_t *q_start,
+                                const longspec_hta_heads *q_out, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/* Attention of chunks of new tokens over the paged cache that holds their
+ * prefix and their own K/V rows (appended before this call): token
+ * q_start[b] + t, at position pos = prefix_len[b] + t, attends to the keys
+ * j <= pos of sequence b, of them the last `window` ones (j > pos - window)
+ * when window > 0.  One token per sequence is a decode step, a whole prompt
+ * a prefill, and ragged chunks mix both in one call.
+ *   dims: B, Hq, Hkv, D, L_cap, scale, T = N tokens (as in append);
+ *   q: rows of Hq heads (stride_b not used, stride_h must be D);
+ *   out bf16 [N][Hq][D], lse fp32 [N][Hq] (natural log);
+ *   workspace: longspec_hta_chunk_workspace_bytes(dims) bytes, 16-byte
+ *   aligned, status word first.
+ * Cache rows outside a sequence's keys, and table entries of blocks that
+ * hold none of the keys its tokens see, are not read as keys (they may hold
+ * anything).  Padding tokens' rows of out and lse are left as they are.
+ * Errors as append; a sequence whose prefix_len is out of range gives NaN
+ * rows, a table entry out of range is read as block 0 and reported. */
+LONGSPEC_HTA_API size_t longspec_hta_chunk_workspace_bytes(const longspec_hta_dims *dims);
+LONGSPEC_HTA_API int longspec_hta_chunk_attention_paged(const longspec_hta_dims *dims,
+                                const longspec_hta_heads *q, const longspec_hta_cache *cache,
+                                const int32_t *prefix_len, const int32_t *q_start, int window,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* longspec_hta_verify_paged, longspec_hta_prefix_attention_paged and
+ * longspec_hta_commit_paged over a cache held in e4m3 (both scales set; a
+ * bf16 cache is INVALID_OPTION here).  k_tree and v_tree stay bf16; the
+ * commit stores the accepted rows in e4m3.  Arguments, results and errors
+ * otherwise as those calls; the attention calls' workspace is
+ * longspec_hta_q8_workspace_bytes(dims). */
+LONGSPEC_HTA_API size_t longspec_hta_q8_workspace_bytes(const longspec_hta_dims *dims);
+LONGSPEC_HTA_API int longspec_hta_verify_paged_q8(const longspec_hta_dims *dims, const void *q,
+                                const longspec_hta_cache *cache, const int32_t *prefix_len,
+                                const void *k_tree, const void *v_tree, const int32_t *parent,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+LONGSPEC_HTA_API int longspec_hta_prefix_attention_paged_q8(const longspec_hta_dims *dims, const void *q,
+                                const longspec_hta_cache *cache, const int32_t *prefix_len,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+LONGSPEC_HTA_API int longspec_hta_commit_paged_q8(const longspec_hta_dims *dims, const longspec_hta_cache *cache,
                                 int32_t *prefix_len, const void *k_tree, const void *v_tree,
                                 const int32_t *accept_len, const int32_t *path, void *workspace,
                                 size_t workspace_bytes, cudaStream_t stream);

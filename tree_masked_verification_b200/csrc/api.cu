@@ -1,4 +1,5 @@
-// api.cu -- the C ABI of liblongspec_hta.so (declared in include/longspec_hta.h).
+// api.cu -- the C ABI of liblongspec_hta.so (declared in include/longspec_hta.h);
+// the calls on new tokens and e4m3 caches are in api_cache.cu.
 //
 // Host side only: argument checks, the split-KV chunking, tensor-map
 // (TMA descriptor) encoding with a small per-pointer cache, and the two
@@ -9,24 +10,22 @@
 #include <mutex>
 
 #include "../../include/longspec_hta.h"
+#include "api_internal.h"
+#include "cache_kernels.h"
 #include "hta_kernels.h"
 
 using hta::PrefixParams;
 using hta::TreeMergeParams;
+using namespace hta_api;
 
 namespace {
-
-// ---------------------------------------------------------------- device
-struct DeviceInfo {
-    bool probed = false;
-    bool supported = false;
-    int num_sms = 0;
-};
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
+}  // namespace
 
-int current_device(DeviceInfo *out) {
+// ---------------------------------------------------------------- device
+int hta_api::current_device(DeviceInfo *out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LONGSPEC_HTA_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return LONGSPEC_HTA_ERR_UNSUPPORTED_DEVICE;
@@ -47,12 +46,7 @@ int current_device(DeviceInfo *out) {
 }
 
 // ------------------------------------------------------------ tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
+EncodeTiledFn hta_api::encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -65,6 +59,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+namespace {
 struct MapKey {
     int dev;
     const void *ptr;
@@ -115,10 +110,10 @@ int tensor_map(const void *ptr, uint64_t rows, int D, CUtensorMap *out, int box_
     return LONGSPEC_HTA_OK;
 }
 
-// ------------------------------------------------------------- validation
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-int check_dims(const longspec_hta_dims *d) {
+// ------------------------------------------------------------- validation
+int hta_api::check_dims(const longspec_hta_dims *d) {
     if (!d) return LONGSPEC_HTA_ERR_NULL_POINTER;
     if (d->B < 1 || d->Hq < 1 || d->Hkv < 1 || d->T < 1 || d->L_cap < 0 || d->Hq % d->Hkv != 0)
         return LONGSPEC_HTA_ERR_INVALID_DIMS;
@@ -132,21 +127,16 @@ int check_dims(const longspec_hta_dims *d) {
     return LONGSPEC_HTA_OK;
 }
 
-float scale_of(const longspec_hta_dims *d) {
+float hta_api::scale_of(const longspec_hta_dims *d) {
     return d->scale > 0.f ? d->scale : 1.f / std::sqrt(static_cast<float>(d->D));
 }
 
-int m_tiles_of(const longspec_hta_dims *d) {
+static int m_tiles_of(const longspec_hta_dims *d) {
     const int M = (d->Hq / d->Hkv) * d->T;
     return (M + 127) / 128;
 }
 
-// Split-KV chunking: chunk_tiles tiles of 128 keys per split, S splits.
-struct Chunking {
-    int S, chunk_tiles;
-};
-
-Chunking chunking_for(const longspec_hta_dims *d, int requested, int num_sms) {
+Chunking hta_api::chunking_for(const longspec_hta_dims *d, int requested, int num_sms) {
     const int tiles = std::max(1, (d->L_cap + hta::kKeyTile - 1) / hta::kKeyTile);
     auto make = [&](int s) {
         s = std::max(1, std::min(std::min(s, tiles), hta::kMaxSplits));
@@ -168,13 +158,7 @@ Chunking chunking_for(const longspec_hta_dims *d, int requested, int num_sms) {
     return best;
 }
 
-struct WsLayout {
-    size_t o_off, lse_off, total;
-};
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-WsLayout ws_layout(const longspec_hta_dims *d, int S) {
+WsLayout hta_api::ws_layout(const longspec_hta_dims *d, int S) {
     const size_t rows = 1ull * d->B * d->Hq * d->T;
     WsLayout w;
     w.o_off = hta::kStatusBytes;
@@ -183,7 +167,7 @@ WsLayout ws_layout(const longspec_hta_dims *d, int S) {
     return w;
 }
 
-PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c, const void *q,
+static PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c, const void *q,
                            const void *kp, const void *vp, const int32_t *plen, float *o_part,
                            float *lse_part, uint32_t *status) {
     PrefixParams p{};
@@ -204,7 +188,7 @@ PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c, const 
     return p;
 }
 
-int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int kernel, cudaEvent_t ev_begin,
+static int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int kernel, cudaEvent_t ev_begin,
                cudaEvent_t ev_end, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     const bool tc = kernel == LONGSPEC_HTA_PREFIX_TCGEN05;
@@ -226,7 +210,7 @@ int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int kernel, cu
     return LONGSPEC_HTA_OK;
 }
 
-TreeMergeParams tree_params(const longspec_hta_dims *d, int mode, int S, const void *q,
+TreeMergeParams hta_api::tree_params(const longspec_hta_dims *d, int mode, int S, const void *q,
                             const void *kt, const void *vt, const int32_t *parent,
                             const int32_t *plen, const float *o_part, const float *lse_part,
                             uint32_t *status) {
@@ -245,8 +229,6 @@ TreeMergeParams tree_params(const longspec_hta_dims *d, int mode, int S, const v
     t.status = status;
     return t;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -276,6 +258,7 @@ const char *longspec_hta_strerror(int code) {
     case LONGSPEC_HTA_ERR_INTERNAL: return "internal kernel precondition failed";
     case LONGSPEC_HTA_ERR_BAD_BLOCK: return "a block_table entry is outside [0, num_blocks)";
     case LONGSPEC_HTA_ERR_BAD_PATH: return "an accepted length or path entry is out of range";
+    case LONGSPEC_HTA_ERR_BAD_RANGES: return "q_start is not ascending inside [0, N]";
     default: return "unknown status";
     }
 }
@@ -763,6 +746,8 @@ int longspec_hta_get_status(void *workspace, cudaStream_t stream) {
     if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(workspace, 0, sizeof(word)) != cudaSuccess)
         return LONGSPEC_HTA_ERR_CUDA;
+    // ranges out of order bring lengths and blocks of the wrong sequence with them
+    if (word & hta::kStatusBadRanges) return LONGSPEC_HTA_ERR_BAD_RANGES;
     if (word & hta::kStatusBadParent) return LONGSPEC_HTA_ERR_BAD_PARENT;
     if (word & hta::kStatusPrefixLenRange) return LONGSPEC_HTA_ERR_PREFIX_LEN_RANGE;
     if (word & hta::kStatusPipelineTimeout) return LONGSPEC_HTA_ERR_PIPELINE_TIMEOUT;

@@ -37,6 +37,7 @@ ERR_PIPELINE_TIMEOUT = -18
 ERR_INTERNAL = -19
 ERR_BAD_BLOCK = -20
 ERR_BAD_PATH = -21
+ERR_BAD_RANGES = -22
 
 PREFIX_TCGEN05 = 0
 PREFIX_SIMT = 1
@@ -54,6 +55,9 @@ EXPORTED = [
     "longspec_hta_accept_workspace_bytes", "longspec_hta_accept_greedy",
     "longspec_hta_commit", "longspec_hta_commit_paged", "longspec_hta_window_verify",
     "longspec_hta_window_workspace_bytes",
+    "longspec_hta_qk_norm_rope", "longspec_hta_append_paged", "longspec_hta_chunk_workspace_bytes",
+    "longspec_hta_chunk_attention_paged", "longspec_hta_q8_workspace_bytes", "longspec_hta_verify_paged_q8",
+    "longspec_hta_prefix_attention_paged_q8", "longspec_hta_commit_paged_q8",
 ]
 
 
@@ -81,6 +85,24 @@ class PagedKV(ctypes.Structure):
     _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("num_blocks", ctypes.c_int),
                 ("block_size", ctypes.c_int), ("max_blocks", ctypes.c_int)]
+
+
+class Cache(ctypes.Structure):
+    """longspec_hta_cache: a paged cache, bf16 or (with scales) e4m3."""
+    _fields_ = PagedKV._fields_ + [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    """longspec_hta_heads: rows of heads at element strides (b, token, head)."""
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """longspec_hta_rope: frequencies and norm weights of query and key heads."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -132,6 +154,17 @@ def load():
             lib.longspec_hta_window_workspace_bytes.argtypes = [pd]
             lib.longspec_hta_window_workspace_bytes.restype = sz
             lib.longspec_hta_commit_paged.argtypes = [pd, pk] + [vp] * 5 + [vp, sz, vp]
+            ph, pr, pc = ctypes.POINTER(Heads), ctypes.POINTER(Rope), ctypes.POINTER(Cache)
+            lib.longspec_hta_qk_norm_rope.argtypes = [ci] * 5 + [ph, ph, vp, pr, ph, ph, vp]
+            lib.longspec_hta_append_paged.argtypes = [pd, ph, ph, ph, pr, pc, vp, vp, ph, vp, sz, vp]
+            lib.longspec_hta_chunk_workspace_bytes.argtypes = [pd]
+            lib.longspec_hta_chunk_workspace_bytes.restype = sz
+            lib.longspec_hta_chunk_attention_paged.argtypes = [pd, ph, pc, vp, vp, ci] + [vp] * 3 + [sz, vp]
+            lib.longspec_hta_q8_workspace_bytes.argtypes = [pd]
+            lib.longspec_hta_q8_workspace_bytes.restype = sz
+            lib.longspec_hta_verify_paged_q8.argtypes = [pd, vp, pc] + [vp] * 7 + [sz, vp]
+            lib.longspec_hta_prefix_attention_paged_q8.argtypes = [pd, vp, pc] + [vp] * 4 + [sz, vp]
+            lib.longspec_hta_commit_paged_q8.argtypes = [pd, pc] + [vp] * 6 + [sz, vp]
             _lib = lib
     return _lib
 
@@ -278,11 +311,33 @@ def _paged_dims(q, k_cache, L_cap, scale):
 
 def verify_paged(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, parent, *, L_cap,
                  out=None, lse=None, workspace=None, scale: float = 0.0, num_splits: int = 0,
-                 prefix_events=None, stream=None):
+                 prefix_events=None, stream=None, k_scale=None, v_scale=None):
     """verify() with the prefix K/V in a paged cache: k/v_cache
     [num_blocks][Hkv][block_size][D], block_table [B][max_blocks] (block ids
-    of each sequence in key order), L_cap the longest prefix allowed."""
+    of each sequence in key order), L_cap the longest prefix allowed.
+
+    With k_scale and v_scale (uint8 [num_blocks][Hkv][block_size]) the caches
+    hold e4m3 codes (see append_paged); the workspace is then one of
+    new_q8_workspace(), and num_splits and prefix_events do not apply."""
     dev = q.device
+    if k_scale is not None or v_scale is not None:
+        _no_prefix_options(num_splits, prefix_events)
+        for t, n in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree")):
+            _need(t, n, torch.bfloat16, dev)
+        _need(prefix_len, "prefix_len", torch.int32, dev)
+        _need(parent, "parent", torch.int32, dev)
+        cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+        dims = _paged_dims(q, k_cache, L_cap, scale)
+        _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree, v_tree, parent)
+        st = _stream_on(dev, stream)
+        out = torch.empty_like(q) if out is None else _result(out, "out", q.shape, torch.bfloat16, dev)
+        lse = (torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None
+               else _result(lse, "lse", q.shape[:3], torch.float32, dev))
+        workspace = new_q8_workspace(dims, dev) if workspace is None else workspace
+        _check(load().longspec_hta_verify_paged_q8(
+            dims, q.data_ptr(), cache, prefix_len.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(),
+            parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
+        return out, lse
     for t, n in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree")):
         _need(t, n, torch.bfloat16, dev)
     _need(prefix_len, "prefix_len", torch.int32, dev)
@@ -305,9 +360,26 @@ def verify_paged(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, p
 
 def prefix_attention_paged(q, k_cache, v_cache, block_table, prefix_len, *, L_cap, out=None,
                            lse=None, workspace=None, scale: float = 0.0, num_splits: int = 0,
-                           prefix_events=None, stream=None):
-    """prefix_attention() with the prefix K/V in a paged cache."""
+                           prefix_events=None, stream=None, k_scale=None, v_scale=None):
+    """prefix_attention() with the prefix K/V in a paged cache, in bf16 or,
+    with k_scale and v_scale, in e4m3 (as in verify_paged)."""
     dev = q.device
+    if k_scale is not None or v_scale is not None:
+        _no_prefix_options(num_splits, prefix_events)
+        _need(q, "q", torch.bfloat16, dev)
+        _need(prefix_len, "prefix_len", torch.int32, dev)
+        cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+        dims = _paged_dims(q, k_cache, L_cap, scale)
+        _tree_shapes(dims, k_cache, prefix_len, block_table)
+        st = _stream_on(dev, stream)
+        out = torch.empty_like(q) if out is None else _result(out, "out", q.shape, torch.bfloat16, dev)
+        lse = (torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None
+               else _result(lse, "lse", q.shape[:3], torch.float32, dev))
+        workspace = new_q8_workspace(dims, dev) if workspace is None else workspace
+        _check(load().longspec_hta_prefix_attention_paged_q8(
+            dims, q.data_ptr(), cache, prefix_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), workspace.nbytes, st))
+        return out, lse
     _need(q, "q", torch.bfloat16, dev)
     _need(prefix_len, "prefix_len", torch.int32, dev)
     kv = _paged(k_cache, v_cache, block_table, dev)
@@ -499,8 +571,28 @@ def commit(k_prefix, v_prefix, prefix_len, k_tree, v_tree, accept_len, path, *, 
 
 
 def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, accept_len, path, *,
-                 L_cap, workspace=None, stream=None):
-    """commit() into a paged cache [num_blocks][Hkv][block_size][D]."""
+                 L_cap, workspace=None, stream=None, k_scale=None, v_scale=None):
+    """commit() into a paged cache [num_blocks][Hkv][block_size][D], in bf16
+    or, with k_scale and v_scale, in e4m3 (the rows are then stored as
+    append_paged stores them)."""
+    if k_scale is not None or v_scale is not None:
+        dev = k_tree.device
+        _need(k_tree, "k_tree", torch.bfloat16, dev)
+        _need(v_tree, "v_tree", torch.bfloat16, dev)
+        for t, n in ((prefix_len, "prefix_len"), (accept_len, "accept_len"), (path, "path")):
+            _need(t, n, torch.int32, dev)
+        cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+        dims = _commit_dims(k_tree, L_cap)
+        _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree, v_tree, path)
+        if tuple(accept_len.shape) != (dims.B,):
+            raise ValueError(f"accept_len must be [{dims.B}]")
+        st = _stream_on(dev, stream)
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        _check(load().longspec_hta_commit_paged_q8(
+            dims, cache, prefix_len.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), accept_len.data_ptr(),
+            path.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
+        return
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_tree, "k_tree"), (v_tree, "v_tree")):
         _need(t, n, torch.bfloat16, k_tree.device)
     for t, n in ((block_table, "block_table"), (prefix_len, "prefix_len"), (accept_len, "accept_len"),
@@ -513,6 +605,259 @@ def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, acce
     _check(load().longspec_hta_commit_paged(ctypes.byref(dims), ctypes.byref(kv), _ptr(prefix_len),
                                             _ptr(k_tree), _ptr(v_tree), _ptr(accept_len), _ptr(path),
                                             _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ---- new tokens: norm, rotation, append, chunk attention; the e4m3 cache ----
+
+def _stream_on(dev, stream) -> int:
+    """The stream to launch on; the tensors must be on the current device."""
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, which is not the current CUDA device")
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev.index:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors are on {dev}")
+    return _stream(stream)
+
+
+def _result(t, name, shape, dtype, dev):
+    _need(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _no_prefix_options(num_splits, prefix_events):
+    if num_splits or prefix_events:
+        raise ValueError("num_splits and prefix_events do not apply to an e4m3 cache")
+
+
+def _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev) -> Cache:
+    dtype = torch.bfloat16
+    if k_scale is not None or v_scale is not None:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache has both k_scale and v_scale")
+        dtype = torch.float8_e4m3fn
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(t, n, torch.uint8, dev)
+            if t.shape != k_cache.shape[:3]:
+                raise ValueError(f"{n} must be [num_blocks][Hkv][block_size]")
+    _need(k_cache, "k_cache", dtype, dev)
+    _need(v_cache, "v_cache", dtype, dev)
+    _need(block_table, "block_table", torch.int32, dev)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or block_table.dim() != 2:
+        raise ValueError("k/v_cache must be [num_blocks][Hkv][block_size][D], block_table [B][max_blocks]")
+    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), shape[0], shape[2],
+                 block_table.shape[1], _ptr(k_scale), _ptr(v_scale))
+
+
+def _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree=None, v_tree=None, nodes=None):
+    if k_cache.shape[1] != dims.Hkv or k_cache.shape[3] != dims.D:
+        raise ValueError(f"the cache holds {k_cache.shape[1]} heads of {k_cache.shape[3]}")
+    if prefix_len.shape != (dims.B,) or block_table.shape[0] != dims.B:
+        raise ValueError(f"prefix_len must be [{dims.B}], block_table [{dims.B}][max_blocks]")
+    if k_tree is not None and (k_tree.shape != (dims.B, dims.Hkv, dims.T, dims.D) or v_tree.shape != k_tree.shape
+                               or nodes.shape != (dims.B, dims.T)):
+        raise ValueError(f"k/v_tree must be [{dims.B}][{dims.Hkv}][{dims.T}][{dims.D}] and the node array "
+                         f"[{dims.B}][{dims.T}]")
+
+
+def _heads(t, name, dev, axes):
+    """Heads of a bf16 tensor whose rows are D contiguous values; axes: its
+    strides' places for (b, token, head), None for no batch axis."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    b, n, h = axes
+    return Heads(t.data_ptr(), 0 if b is None else st[b], st[n], st[h])
+
+
+_TOKENS, _BATCHED = (None, 0, 1), (0, 2, 1)     # [N][H][D] and [B][H][T][D]
+
+
+def _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev) -> Rope:
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
+        raise ValueError(f"inv_freq must be [rot_dim / 2] with rot_dim from 2 to {D}")
+    if not rope_scale > 0:
+        raise ValueError("rope_scale must be above 0")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, n, torch.bfloat16, dev)
+            if w.shape != (D,):
+                raise ValueError(f"{n} must be [{D}]")
+    return Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, _ptr(q_weight),
+                _ptr(k_weight), eps)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norm (where there are weights) and rotation of query and key heads.
+
+    q [N][Hq][D] and k [N][Hkv][D] with positions int32 [N], or
+    [B][Hq][T][D] and [B][Hkv][T][D] with positions [B][T]; bf16 views of any
+    strides whose heads are contiguous, so slices of a projection's rows are
+    taken as they are.  inv_freq fp32 [rot_dim/2]: the first rot_dim values of
+    a head are turned, as pairs (i, i + rot_dim/2) or, interleaved,
+    (2i, 2i + 1).  For contexts stretched beyond training pass the stretched
+    frequencies and, as rope_scale, the factor on cos and sin that goes with
+    them.  Returns (q_out, k_out), contiguous unless given; q_out=q, k_out=k
+    works in place."""
+    dev = q.device
+    if q.dim() != k.dim() or q.dim() not in (3, 4):
+        raise ValueError("q and k must be [N][H][D] or [B][H][T][D]")
+    axes = _TOKENS if q.dim() == 3 else _BATCHED
+    shape, ks = q.shape, k.shape
+    if q.dim() == 3:
+        B, T, Hq, Hkv, D = 1, shape[0], shape[1], ks[1], shape[2]
+        same, want = ks[0] == T, (T,)
+    else:
+        B, T, Hq, Hkv, D = shape[0], shape[2], shape[1], ks[1], shape[3]
+        same, want = ks[0] == B and ks[2] == T, (B, T)
+    if not same or ks[-1] != D:
+        raise ValueError(f"q {list(shape)} and k {list(ks)} do not belong together")
+    _need(positions, "positions", torch.int32, dev)
+    if positions.shape != want:
+        raise ValueError(f"positions must be {list(want)}, got {list(positions.shape)}")
+    rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev)
+    st = _stream_on(dev, stream)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    elif q_out.shape != shape:
+        raise ValueError(f"q_out must be {list(shape)}")
+    if k_out is None:
+        k_out = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+    elif k_out.shape != ks:
+        raise ValueError(f"k_out must be {list(ks)}")
+    _check(load().longspec_hta_qk_norm_rope(
+        B, T, Hq, Hkv, D, _heads(q, "q", dev, axes), _heads(k, "k", dev, axes), positions.data_ptr(), rope,
+        _heads(q_out, "q_out", dev, axes), _heads(k_out, "k_out", dev, axes), st))
+    return q_out, k_out
+
+
+def _ragged(prefix_len, q_start, block_table, dev):
+    _need(prefix_len, "prefix_len", torch.int32, dev)
+    _need(q_start, "q_start", torch.int32, dev)
+    B = prefix_len.shape[0] if prefix_len.dim() == 1 else 0
+    if B < 1 or q_start.shape != (B + 1,) or block_table.shape[0] != B:
+        raise ValueError("prefix_len must be [B], q_start [B + 1], block_table [B][max_blocks]")
+    return B
+
+
+def _append(q, k, v, rope, k_cache, v_cache, block_table, prefix_len, q_start, L_cap, k_scale, v_scale, q_out,
+            workspace, stream):
+    dev = k.device
+    N, Hkv, D = k.shape
+    if v.shape != k.shape or (q is not None and (q.dim() != 3 or q.shape[0] != N or q.shape[2] != D)):
+        raise ValueError("k and v must be [N][Hkv][D], q [N][Hq][D]")
+    if k_cache.dim() != 4 or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+        raise ValueError(f"the cache must be [num_blocks][{Hkv}][block_size][{D}]")
+    cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+    B = _ragged(prefix_len, q_start, block_table, dev)
+    st = _stream_on(dev, stream)
+    qh = oh = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        elif q_out.shape != q.shape:
+            raise ValueError(f"q_out must be {list(q.shape)}")
+        qh, oh = _heads(q, "q", dev, _TOKENS), _heads(q_out, "q_out", dev, _TOKENS)
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+    _check(load().longspec_hta_append_paged(
+        Dims(B, Hkv if q is None else q.shape[1], Hkv, D, N, L_cap, 0.0), qh, _heads(k, "k", dev, _TOKENS),
+        _heads(v, "v", dev, _TOKENS), rope, cache, prefix_len.data_ptr(), q_start.data_ptr(), oh,
+        workspace.data_ptr(), workspace.nbytes, st))
+    return q_out
+
+
+def append_paged(k, v, k_cache, v_cache, block_table, prefix_len, q_start, *, L_cap, k_scale=None, v_scale=None,
+                 workspace=None, stream=None):
+    """Append new tokens' K/V rows [N][Hkv][D] (views of any strides whose
+    heads are contiguous) to a paged cache: rows q_start[b] .. q_start[b+1]-1
+    go to positions prefix_len[b] .. of sequence b (q_start int32 [B+1],
+    ascending; rows from q_start[B] on are padding).  prefix_len is not
+    advanced.
+
+    The cache is bf16, or e4m3 with a scale byte e per row in k_scale and
+    v_scale (uint8 [num_blocks][Hkv][block_size]): a row is kept as codes
+    times 2^(e - 127), the smallest power of two under which the row's
+    largest value stays within 448 (e clamped to [16, 134]; a row with an
+    infinity or a NaN reads back as NaN).  Problems on the device
+    (lengths past L_cap, bad blocks, ranges out of order) leave those rows
+    unwritten and show in get_status(workspace); workspace: at least 256
+    bytes, zeroed."""
+    _append(None, k, v, None, k_cache, v_cache, block_table, prefix_len, q_start, L_cap, k_scale, v_scale, None,
+            workspace, stream)
+
+
+def rope_append_paged(q, k, v, inv_freq, k_cache, v_cache, block_table, prefix_len, q_start, *, L_cap,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                      rope_scale: float = 1.0, k_scale=None, v_scale=None, q_out=None, workspace=None,
+                      stream=None):
+    """append_paged() with the norm and rotation of qk_norm_rope() in the same
+    pass: q and k are normed and rotated at their positions
+    prefix_len[b] + place in the chunk, k and v go to the cache.  Returns
+    q_out [N][Hq][D]; padding rows of it are left as they were."""
+    rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, k.shape[-1], k.device)
+    return _append(q, k, v, rope, k_cache, v_cache, block_table, prefix_len, q_start, L_cap, k_scale, v_scale, q_out,
+                   workspace, stream)
+
+
+def new_chunk_workspace(q, k_cache, B: int, *, L_cap: int) -> torch.Tensor:
+    """A zeroed workspace for chunk_attention_paged calls of q's shape."""
+    N, Hq, D = q.shape
+    n = load().longspec_hta_chunk_workspace_bytes(Dims(B, Hq, k_cache.shape[1], D, N, L_cap, 0.0))
+    if n == 0:
+        raise HtaError(ERR_INVALID_DIMS)
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def chunk_attention_paged(q, k_cache, v_cache, block_table, prefix_len, q_start, *, L_cap, window: int = 0,
+                          k_scale=None, v_scale=None, scale: float = 0.0, out=None, lse=None, workspace=None,
+                          stream=None):
+    """Causal attention of chunks of new tokens over the paged cache that
+    holds them (append_paged / rope_append_paged before this call).
+
+    q [N][Hq][D] bf16 (tokens at any stride): rows q_start[b] ..
+    q_start[b+1]-1 are at positions prefix_len[b] .. of sequence b and attend
+    to its keys up to their own position, to the last `window` of them when
+    window > 0.  Single tokens (a decode step), whole prompts and ragged
+    mixtures are all such chunks.  The cache is bf16, or e4m3 with scales.
+    Returns (out bf16 [N][Hq][D], lse fp32 [N][Hq]); padding rows (from
+    q_start[B] on) are left as they were."""
+    dev = q.device
+    N, Hq, D = q.shape
+    if k_cache.dim() != 4 or k_cache.shape[3] != D or Hq % k_cache.shape[1]:
+        raise ValueError(f"the cache must be [num_blocks][Hkv][block_size][{D}] with Hkv dividing {Hq}")
+    cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+    B = _ragged(prefix_len, q_start, block_table, dev)
+    st = _stream_on(dev, stream)
+    qh = _heads(q, "q", dev, _TOKENS)
+    if qh.stride_h != D:
+        raise ValueError("q: the heads of a token must be contiguous")
+    out = (torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev) if out is None
+           else _result(out, "out", (N, Hq, D), torch.bfloat16, dev))
+    lse = (torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse is None
+           else _result(lse, "lse", (N, Hq), torch.float32, dev))
+    if workspace is None:
+        workspace = new_chunk_workspace(q, k_cache, B, L_cap=L_cap)
+    _check(load().longspec_hta_chunk_attention_paged(
+        Dims(B, Hq, k_cache.shape[1], D, N, L_cap, scale), qh, cache, prefix_len.data_ptr(), q_start.data_ptr(),
+        window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
+    return out, lse
+
+
+def new_q8_workspace(dims: Dims, device=None) -> torch.Tensor:
+    """A zeroed workspace for verify_paged / prefix_attention_paged over an
+    e4m3 cache."""
+    n = load().longspec_hta_q8_workspace_bytes(dims)
+    if n == 0:
+        raise HtaError(ERR_INVALID_DIMS)
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
 
 
 def selftest_wait_timeout(workspace: torch.Tensor, stream=None) -> int:
