@@ -86,6 +86,62 @@ void set_rope(hta::RowsParams *p, const longspec_hta_rope *r) {
     p->k_weight = static_cast<const __nv_bfloat16 *>(r->k_weight);
 }
 
+// Workspace of the attention calls: status word, partial headers, and two
+// slots of up to 256 rows per CTA (chunk_tc.cu).
+struct SlotLayout {
+    int slot_rows;
+    size_t heads_off, o_off, lse_off, total;
+};
+SlotLayout slot_layout(long long packed_rows, int D, int grid) {
+    SlotLayout l;
+    l.slot_rows = static_cast<int>(packed_rows < 256 ? packed_rows : 256);
+    l.heads_off = hta::kStatusBytes;
+    l.o_off = align256(l.heads_off + 2 * sizeof(hta::PartHead) * grid);
+    l.lse_off = align256(l.o_off + 2ull * grid * l.slot_rows * D * sizeof(float));
+    l.total = align256(l.lse_off + 2ull * grid * l.slot_rows * sizeof(float));
+    return l;
+}
+
+// The bf16 cache as [num_blocks * Hkv * block_size][D] in boxes of one block's
+// rows by 64 columns, 128-byte swizzle.
+int cache_map(const void *base, const longspec_hta_cache *c, int Hkv, int D, CUtensorMap *out) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return LONGSPEC_HTA_ERR_CUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D),
+                                static_cast<cuuint64_t>(c->num_blocks) * Hkv * c->block_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(c->block_size)}, es[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
+}
+
+// The common part of the attention calls: p holds the rows, the lengths and
+// the outputs already.
+int run_attention(hta::ChunkParams &p, const longspec_hta_dims *d, const longspec_hta_cache *cache, void *workspace,
+                  int num_sms, cudaStream_t stream) {
+    p.B = d->B; p.Hq = d->Hq; p.Hkv = d->Hkv; p.G = d->Hq / d->Hkv; p.D = d->D;
+    p.N = d->T;
+    p.L_cap = d->L_cap;
+    p.scale_log2 = scale_of(d) * hta::kLog2e;
+    p.cache = view_of(cache);
+    p.grid = num_sms;
+    const SlotLayout l = slot_layout(1LL * p.G * d->T, d->D, p.grid);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.slot_rows = l.slot_rows;
+    p.status = reinterpret_cast<uint32_t *>(ws);
+    p.heads = reinterpret_cast<hta::PartHead *>(ws + l.heads_off);
+    p.o_part = reinterpret_cast<float *>(ws + l.o_off);
+    p.lse_part = reinterpret_cast<float *>(ws + l.lse_off);
+    CUtensorMap tk{}, tv{};
+    if (!cache->k_scale) {
+        HTA_TRY(cache_map(cache->k_cache, cache, d->Hkv, d->D, &tk));
+        HTA_TRY(cache_map(cache->v_cache, cache, d->Hkv, d->D, &tv));
+    }
+    return hta::launch_chunk_tc(p, tk, tv, stream) == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA; }
 
 }  // namespace
@@ -157,8 +213,9 @@ int longspec_hta_append_paged(const longspec_hta_dims *dims, const longspec_hta_
 }
 
 size_t longspec_hta_chunk_workspace_bytes(const longspec_hta_dims *dims) {
-    if (check_token_dims(dims) != LONGSPEC_HTA_OK) return 0;
-    return hta::kStatusBytes;
+    DeviceInfo di;
+    if (check_token_dims(dims) != LONGSPEC_HTA_OK || current_device(&di) != LONGSPEC_HTA_OK) return 0;
+    return slot_layout(1LL * (dims->Hq / dims->Hkv) * dims->T, dims->D, di.num_sms).total;
 }
 
 int longspec_hta_chunk_attention_paged(const longspec_hta_dims *dims, const longspec_hta_heads *q,
@@ -170,35 +227,30 @@ int longspec_hta_chunk_attention_paged(const longspec_hta_dims *dims, const long
     HTA_TRY(check_ints(prefix_len));
     HTA_TRY(check_ints(q_start));
     if (window < 0) return LONGSPEC_HTA_ERR_INVALID_OPTION;
-    DeviceInfo di;
-    HTA_TRY(check_workspace(workspace, workspace_bytes, longspec_hta_chunk_workspace_bytes(dims)));
+    HTA_TRY(check_workspace(workspace, workspace_bytes, hta::kStatusBytes));
     if (dims->T == 0) return LONGSPEC_HTA_OK;
     HTA_TRY(check_heads(q));
     if (q->stride_h != dims->D) return LONGSPEC_HTA_ERR_INVALID_OPTION;
     if (!out || !lse) return LONGSPEC_HTA_ERR_NULL_POINTER;
     if (!aligned16(out) || !aligned4(lse)) return LONGSPEC_HTA_ERR_MISALIGNED;
+    DeviceInfo di;
     HTA_TRY(current_device(&di));
+    HTA_TRY(check_workspace(workspace, workspace_bytes, longspec_hta_chunk_workspace_bytes(dims)));
     hta::ChunkParams p{};
-    p.B = dims->B; p.Hq = dims->Hq; p.Hkv = dims->Hkv; p.G = dims->Hq / dims->Hkv; p.D = dims->D;
-    p.N = dims->T;
-    p.L_cap = dims->L_cap;
     p.window = window;
-    p.scale_log2 = scale_of(dims) * hta::kLog2e;
     p.q = static_cast<const __nv_bfloat16 *>(q->p);
     p.q_stride = q->stride_t;
-    p.cache = view_of(cache);
     p.prefix_len = prefix_len;
     p.q_start = q_start;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
-    p.S = 1;
-    p.status = static_cast<uint32_t *>(workspace);
-    return done(hta::launch_chunk_simt(p, stream));
+    return run_attention(p, dims, cache, workspace, di.num_sms, stream);
 }
 
 size_t longspec_hta_q8_workspace_bytes(const longspec_hta_dims *dims) {
-    if (check_dims(dims) != LONGSPEC_HTA_OK) return 0;
-    return ws_layout(dims, 1).total;
+    DeviceInfo di;
+    if (check_dims(dims) != LONGSPEC_HTA_OK || current_device(&di) != LONGSPEC_HTA_OK) return 0;
+    return slot_layout(1LL * (dims->Hq / dims->Hkv) * dims->T, dims->D, di.num_sms).total;
 }
 
 static int run_q8(const longspec_hta_dims *dims, const void *q, const longspec_hta_cache *cache,
@@ -217,27 +269,17 @@ static int run_q8(const longspec_hta_dims *dims, const void *q, const longspec_h
     DeviceInfo di;
     HTA_TRY(current_device(&di));
     HTA_TRY(check_workspace(workspace, workspace_bytes, longspec_hta_q8_workspace_bytes(dims)));
-    const WsLayout w = ws_layout(dims, 1);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     hta::ChunkParams p{};
-    p.B = dims->B; p.Hq = dims->Hq; p.Hkv = dims->Hkv; p.G = dims->Hq / dims->Hkv; p.D = dims->D;
-    p.N = dims->T;
-    p.L_cap = dims->L_cap;
     p.tree = 1;
-    p.scale_log2 = scale_of(dims) * hta::kLog2e;
+    p.tree_tiles = prefix_only ? 0 : (dims->T + 127) / 128;
     p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.cache = view_of(cache);
     p.prefix_len = prefix_len;
-    p.S = 1;
-    p.o_part = reinterpret_cast<float *>(ws + w.o_off);
-    p.lse_part = reinterpret_cast<float *>(ws + w.lse_off);
-    p.status = reinterpret_cast<uint32_t *>(ws);
-    HTA_TRY(done(hta::launch_chunk_simt(p, stream)));
-    hta::TreeMergeParams t = tree_params(dims, prefix_only ? hta::kTreeModePrefixOnly : hta::kTreeModeMerge, 1, q,
-                                         k_tree, v_tree, parent, prefix_len, p.o_part, p.lse_part, p.status);
-    t.out = static_cast<__nv_bfloat16 *>(out);
-    t.lse = lse;
-    return done(hta::launch_tree_merge(t, stream));
+    p.k_tree = static_cast<const __nv_bfloat16 *>(k_tree);
+    p.v_tree = static_cast<const __nv_bfloat16 *>(v_tree);
+    p.parent = parent;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    return run_attention(p, dims, cache, workspace, di.num_sms, stream);
 }
 
 int longspec_hta_verify_paged_q8(const longspec_hta_dims *dims, const void *q, const longspec_hta_cache *cache,

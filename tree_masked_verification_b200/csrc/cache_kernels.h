@@ -74,26 +74,42 @@ struct CommitQ8Params {
 };
 cudaError_t launch_commit_q8(const CommitQ8Params &p, cudaStream_t stream);
 
+// Which rows a partial of chunk_tc_kernel belongs to.
+struct PartHead {
+    int b, kvh, r0, rows;             // rows 0: the slot is empty
+    int s0, last, pad0, pad1;         // last: the item's last segment
+};
+
 // Attention of query rows to a paged cache.  Two row layouts:
 //   chunk (tree = 0): q [N][Hq][D] (token stride q_stride), token t of
 //     sequence b at position prefix_len[b] + t, sees keys (pos - window, pos];
-//   tree  (tree = 1): q [B][Hq][T][D], every row of b sees keys [0, prefix_len[b]).
-// Output row = token*Hq + h (chunk) or (b*Hq + h)*T + t (tree); S > 1 or
-// tree: fp32 partials [rows][S][D], [rows][S] instead of out/lse.
+//   tree  (tree = 1): q [B][Hq][N][D], every row of b sees keys [0, prefix_len[b])
+//     and, with tree_tiles = ceil(N / 128) > 0, its node's ancestors and
+//     itself among the tree's keys k_tree, v_tree [B][Hkv][N][D].
+// Output row = token*Hq + h (chunk) or (b*Hq + h)*N + t (tree).
 struct ChunkParams {
-    int B, Hq, Hkv, G, D, N, L_cap, window, tree;
+    int B, Hq, Hkv, G, D, N, L_cap, window, tree, tree_tiles;
     float scale_log2;
     const __nv_bfloat16 *q;
     long long q_stride;
     CacheView cache;
     const int32_t *prefix_len, *q_start;
+    const __nv_bfloat16 *k_tree, *v_tree;
+    const int32_t *parent;
     __nv_bfloat16 *out;
     float *lse;
-    int S;
-    float *o_part, *lse_part;
     uint32_t *status;
+    // schedule and partials (chunk_tc.cu): grid CTAs, two slots of slot_rows
+    // rows each
+    int grid, slot_rows;
+    int c0, c1, c2, min_share;        // units of work: an item, a key tile of one / two row tiles; least share of a CTA
+    PartHead *heads;                  // [2 * grid]
+    float *o_part, *lse_part;         // [2 * grid][slot_rows][D], [2 * grid][slot_rows]
 };
-cudaError_t launch_chunk_simt(const ChunkParams &p, cudaStream_t stream);
+// tm_k / tm_v: the caches as [num_blocks*Hkv*block_size][D], box 64 x
+// block_size, 128B swizzle (bf16 caches; not used for e4m3 ones)
+cudaError_t launch_chunk_tc(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                            cudaStream_t stream);
 
 // -------------------------------------------------------------- device parts
 // The sequence of token i: the largest b with q_start[b] <= i, run by a whole

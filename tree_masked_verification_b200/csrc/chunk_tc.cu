@@ -1,0 +1,1229 @@
+// chunk_tc.cu -- attention of query rows to a paged cache, bf16 or e4m3, on
+// sm_100a tensor cores: causal chunks of new tokens (ragged, windowed, from
+// one token to whole prompts), and the rows of a draft tree over an e4m3
+// cache followed by the tree's own keys.
+//
+//   o = sum_j e^{x_j} v_j / sum_j e^{x_j},  x_j = scale * q.k_j over the keys
+//   a row sees; one pass with a running maximum m and sum l of 2^{x - m}.
+//
+// Items.  The G query heads of a KV head share its keys, so the rows of a
+// (sequence, KV head) are packed (chunk: r = t*G + g, tree: r = g*T + t) and
+// cut into items of up to 256 rows: two 128-row MMA tiles that share every
+// K/V tile they read (one tile when at most 128 rows are left).  An item's
+// keys come in tiles of 128.
+//
+// Schedule.  Lengths are known to the device only, so every CTA (one per SM)
+// computes the work of all items in units (c0 + tiles * c1 or c2) and takes
+// an equal, contiguous range of the whole: long axes are split over as many
+// CTAs as it takes and ragged batches balance, without a plan kernel or a
+// host copy.  An item that lies in one CTA's range is finished there; one
+// that crosses a border leaves normalised fp32 partials and their lse, at
+// most two per CTA (its first and its last item), which merge_kernel joins.
+//
+// Warps: 0 TMA producer of K, 1 MMA issuer, 2 TMA producer of V (bf16
+// caches), 3 fixer of partly visible V tiles, 4-7 and 8-11 two softmax groups
+// (one row per thread), 12-15 (e4m3 caches) loaders, which read codes into
+// registers one tile ahead, scale them exactly to bf16 and write the
+// swizzled tiles the MMAs read.  With two row tiles group g owns tile g and
+// runs every key tile; with one, group g runs the key tiles j = g mod 2 into
+// an accumulator of its own and the two are merged at the end (the lse merge
+// of two key ranges).  Steps s of an item: group s & 1, key tile
+// s >> (two row tiles); MMA order QK_0 QK_1 [PV_0 QK_2] [PV_1 QK_3] ...
+//
+// Tensor memory: S[g] columns 128g.. (fp32 scores; P as bf16 pairs over its
+// first 64), O[g] columns 256 + gD...  P is rounded to bf16 for the tensor
+// cores (relative 2^-9 on average, the same size as the output's own
+// rounding); its sum l, the maximum and O stay in fp32.  The running maximum
+// moves only when it grew by more than 2^8 (exact after the division by l).
+//
+// Keys a row does not see: scores are set to -inf, and rows of V that no row
+// of the item may see are zeroed in shared memory (a cache row behind the
+// last key may hold anything).  A V row that some rows see and others do not
+// is zeroed too if it holds an infinity or NaN, and the rows that see it
+// come out as NaN: 0 * inf would otherwise reach the others.
+#include "cache_kernels.h"
+
+namespace hta {
+
+namespace {
+
+constexpr int kItemRows = 256;
+constexpr int kPoisonRing = 8;
+
+template <int D, bool Q8>
+struct Cfg {
+    static constexpr int NK = D == 128 ? 3 : 4;             // K ring depth
+    static constexpr int NV = D == 128 ? 2 : 4;             // V ring depth
+    static constexpr int HALVES = D / 64;                   // 64-column swizzle boxes
+    static constexpr int BOX = 128 * 64 * 2;
+    static constexpr int TILE = 128 * D * 2;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * TILE;
+    static constexpr int OFF_V = OFF_K + NK * TILE;
+    static constexpr int OFF_BAR = OFF_V + NV * TILE;
+    // q_full, q_empty, o_full, o_empty, drain, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], v_fix[NV],
+    // s_full[2], p_ready[2]
+    static constexpr int NUM_BARS = 5 + 2 * NK + 3 * NV + 4;
+    static constexpr int OFF_POISON = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // [kPoisonRing][4] words
+    static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort, walk start (b, kvh, tile), at, end
+    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // int32 [kTMax] (trees)
+    static constexpr int SMEM = OFF_PARENT + kTMax * 4;
+    static constexpr int SMEM_ALLOC = SMEM + 1024;          // slack to align the base to 1024
+    static constexpr int OFF_XCH = TILE;                    // [2][2][128] floats, in the unused second Q tile
+    static constexpr int OFF_PLAN = OFF_K;                  // int64 per 32 sequences, before the first copy
+    static constexpr int THREADS = Q8 ? 512 : 384;
+    // registers per thread: launch budget 65536 / THREADS (a multiple of 8)
+    static constexpr int REGS_SOFTMAX = Q8 ? 176 : 224;
+    static constexpr int REGS_LOAD = 96;
+    static constexpr int REGS_OTHER = Q8 ? 64 : 56;
+    static_assert(256 * REGS_SOFTMAX + (Q8 ? 128 * REGS_LOAD : 0) + 128 * REGS_OTHER <= THREADS * (Q8 ? 128 : 168),
+                  "register split must fit the launch allocation");
+    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false);
+    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
+    static constexpr int COL_S = 0, COL_O = 256;
+};
+
+constexpr int kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpFix = 3, kWarpSoftmax = 4, kWarpLoad = 12;
+
+// ------------------------------------------------------------ small helpers
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"(n), "r"(pred ? 1u : 0u) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// NaN if any operand is (a NaN score must not get lost in the clamps below)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x for a pair on the FMA pipe (part of the load off the exp2 unit): n =
+// round(x) by the 1.5 * 2^23 addition, 2^(x - n) by the cubic fitted in
+// fit_exp2_poly.py (relative 7.5e-5), n into the exponent.  x is clamped to
+// >= -125: 2^-125 is nothing beside the row's largest term (and a row that
+// sees no key is recognised by its maximum, not by its sum).
+__device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
+    constexpr float kRound = 12582912.0f;
+    float2 v = unf2(x2);
+    v.x = fmaxf(v.x, -125.f);
+    v.y = fmaxf(v.y, -125.f);
+    const uint64_t xc = f2(v.x, v.y);
+    const uint64_t t = add2(xc, f2(kRound, kRound));
+    const uint64_t n = add2(t, f2(-kRound, -kRound));
+    const uint64_t fr = fma2(n, f2(-1.f, -1.f), xc);
+    uint64_t q = fma2(fr, f2(0.05517132207751274f, 0.05517132207751274f),
+                      f2(0.24261054396629333f, 0.24261054396629333f));
+    q = fma2(fr, q, f2(0.6932609677314758f, 0.6932609677314758f));
+    q = fma2(fr, q, f2(0.9999281167984009f, 0.9999281167984009f));
+    const float2 qq = unf2(q), tt = unf2(t);
+    float2 o;
+    o.x = __int_as_float(__float_as_int(qq.x) + (__float_as_int(tt.x) << 23));
+    o.y = __int_as_float(__float_as_int(qq.y) + (__float_as_int(tt.y) << 23));
+    return o;
+}
+
+// bits [lo, hi) of a 32-bit word (lo, hi any integers)
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    const int h = min(max(hi, 0), 32), l = min(max(lo, 0), 32);
+    const uint32_t below_h = h == 0 ? 0u : 0xffffffffu >> (32 - h);
+    const uint32_t below_l = l == 0 ? 0u : 0xffffffffu >> (32 - l);
+    return below_h & ~below_l;
+}
+
+// --------------------------------------------------------------- work items
+struct Seq {
+    int s0, n, L, rows, tiles;      // first token, tokens, prefix, packed rows, items per KV head
+    bool bad;                       // prefix length out of range: rows come out as NaN
+};
+
+__device__ __forceinline__ Seq load_seq(const ChunkParams &p, int b) {
+    Seq s;
+    s.L = p.prefix_len[b];
+    if (p.tree) {
+        s.s0 = 0;
+        s.n = p.N;
+        s.bad = s.L < 0 || s.L > p.L_cap;
+    } else {
+        s.s0 = p.q_start[b];
+        const int s1 = p.q_start[b + 1];
+        s.n = (s.s0 < 0 || s1 < s.s0 || s1 > p.N) ? 0 : s1 - s.s0;   // (reported by check_ranges)
+        s.bad = s.L < 0 || s.L > p.L_cap || s.n > p.L_cap - s.L;
+    }
+    s.rows = s.n * p.G;
+    s.tiles = (s.rows + kItemRows - 1) / kItemRows;
+    return s;
+}
+
+struct Item {
+    int r0, rows;                   // packed rows [r0, r0 + rows)
+    int two;                        // more than one 128-row tile
+    int lo, hi, base;               // cache keys any row may see; first key of tile 0 (whole blocks)
+    int all_lo, all_hi;             // keys every row sees
+    int cache_tiles, nt;            // key tiles from the cache, and with the tree's
+};
+
+__device__ __forceinline__ Item item_of(const ChunkParams &p, const Seq &s, int tile) {
+    Item it;
+    it.r0 = tile * kItemRows;
+    it.rows = min(kItemRows, s.rows - it.r0);
+    it.two = it.rows > 128 ? 1 : 0;
+    it.lo = it.all_lo = 0;
+    if (s.bad) {
+        it.hi = it.all_hi = 0;
+    } else if (p.tree) {
+        it.hi = it.all_hi = s.L;
+    } else {
+        const int t0 = it.r0 / p.G, t1 = (it.r0 + it.rows - 1) / p.G;
+        it.all_hi = s.L + t0 + 1;
+        it.hi = s.L + t1 + 1;
+        if (p.window > 0) {
+            it.lo = max(0, s.L + t0 - p.window + 1);
+            it.all_lo = max(0, s.L + t1 - p.window + 1);
+        }
+    }
+    it.base = it.lo / p.cache.block_size * p.cache.block_size;
+    it.cache_tiles = (it.hi - it.base + 127) / 128;
+    it.nt = it.cache_tiles + p.tree_tiles;
+    if (it.nt == 0) it.nt = it.cache_tiles = 1;        // no key at all: one tile, wholly masked
+    return it;
+}
+
+__device__ __forceinline__ int item_cost(const ChunkParams &p, const Item &it) {
+    return p.c0 + it.nt * (it.two ? p.c2 : p.c1);
+}
+
+// cost of the sequence of each lane (lanes without one: n = 0), for one KV head
+__device__ __forceinline__ long long seq_costs(const ChunkParams &p, const Seq &s) {
+    const int lane = threadIdx.x & 31;
+    long long cost = 0;
+    const bool big = s.tiles > 2;
+    if (!big)
+        for (int i = 0; i < s.tiles; ++i) cost += item_cost(p, item_of(p, s, i));
+    for (uint32_t m = __ballot_sync(0xffffffffu, big); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        Seq o;
+        o.s0 = 0;
+        o.n = 0;
+        o.L = __shfl_sync(0xffffffffu, s.L, src);
+        o.rows = __shfl_sync(0xffffffffu, s.rows, src);
+        o.tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+        o.bad = __shfl_sync(0xffffffffu, s.bad ? 1 : 0, src) != 0;
+        long long c = 0;
+        for (int i = lane; i < o.tiles; i += 32) c += item_cost(p, item_of(p, o, i));
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) c += __shfl_xor_sync(0xffffffffu, c, k);
+        if (lane == src) cost = c;
+    }
+    return cost;
+}
+
+__device__ __forceinline__ long long scan_add(long long v) {     // inclusive, over the warp
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, v, k);
+        if (lane >= k) v += o;
+    }
+    return v;
+}
+
+struct Start {
+    int b, kvh, tile, pad;
+    long long at, begin, end;       // units: start of that item, this CTA's range
+};
+
+// Where this CTA's range of the work begins (the whole CTA calls; `plan` is
+// shared scratch of one int64 per 32 sequences).
+__device__ void plan_start(const ChunkParams &p, long long *plan, Start *out) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int groups = (p.B + 31) / 32;
+    auto lane_seq = [&](int g) {
+        Seq s = {};
+        if (g * 32 + lane < p.B) s = load_seq(p, g * 32 + lane);
+        return s;
+    };
+    for (int g = warp; g < groups; g += warps) {
+        const long long c = scan_add(seq_costs(p, lane_seq(g)));
+        if (lane == 31) plan[g] = c;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long total = 0;
+        for (int g = lane; g < groups; g += 32) total += plan[g];
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+        const long long work = total * p.Hkv;
+        const long long share = max((work + gridDim.x - 1) / gridDim.x, static_cast<long long>(p.min_share));
+        const long long begin = share * blockIdx.x, end = min(work, begin + share);
+        Start st = {p.B, 0, 0, 0, 0, begin, end};
+        if (begin < work) {
+            long long before = 0;                       // of the KV-head-0 axis
+            int g = 0;
+            for (;; g += 32) {
+                const long long c = g + lane < groups ? plan[g + lane] : 0;
+                const long long cum = before + scan_add(c);
+                const uint32_t past = __ballot_sync(0xffffffffu, cum * p.Hkv > begin);
+                if (past) {
+                    const int k = __ffs(past) - 1;
+                    before = __shfl_sync(0xffffffffu, cum - c, k);
+                    g += k;
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, cum, 31);
+            }
+            const Seq s = lane_seq(g);
+            const long long c = seq_costs(p, s);
+            const long long cum = before + scan_add(c);
+            const int k = __ffs(__ballot_sync(0xffffffffu, cum * p.Hkv > begin)) - 1;
+            Seq o;
+            o.s0 = o.n = 0;
+            o.L = __shfl_sync(0xffffffffu, s.L, k);
+            o.rows = __shfl_sync(0xffffffffu, s.rows, k);
+            o.tiles = __shfl_sync(0xffffffffu, s.tiles, k);
+            o.bad = __shfl_sync(0xffffffffu, s.bad ? 1 : 0, k) != 0;
+            const long long cost = __shfl_sync(0xffffffffu, c, k);
+            before = __shfl_sync(0xffffffffu, cum - c, k) * p.Hkv;
+            st.b = g * 32 + k;
+            st.kvh = static_cast<int>((begin - before) / cost);
+            before += cost * st.kvh;
+            for (int t = 0;; t += 32) {
+                const long long ic = t + lane < o.tiles ? item_cost(p, item_of(p, o, t + lane)) : 0;
+                const long long icum = before + scan_add(ic);
+                const uint32_t past = __ballot_sync(0xffffffffu, icum > begin);
+                if (past) {
+                    const int i = __ffs(past) - 1;
+                    st.tile = t + i;
+                    st.at = __shfl_sync(0xffffffffu, icum - ic, i);
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, icum, 31);
+            }
+        }
+        if (lane == 0) *out = st;
+    }
+    __syncthreads();
+}
+
+// The items of this CTA's range, in order; every role walks them alike.
+struct Walk {
+    int b, kvh, tile;
+    long long at, begin, end;
+    Seq s;
+    Item it;
+    int cur_kvh, cur_b;             // of `it`
+    int j0, j1;                     // this CTA's key tiles of `it`
+
+    __device__ __forceinline__ void start(const ChunkParams &p, const Start *st) {
+        b = st->b;
+        kvh = st->kvh;
+        tile = st->tile;
+        at = st->at;
+        begin = st->begin;
+        end = st->end;
+        if (b < p.B) s = load_seq(p, b);
+    }
+    __device__ __forceinline__ bool next(const ChunkParams &p) {
+        for (;;) {
+            if (b >= p.B || at >= end) return false;
+            if (tile >= s.tiles) {
+                tile = 0;
+                if (s.tiles == 0 || ++kvh >= p.Hkv) {
+                    kvh = 0;
+                    if (++b >= p.B) return false;
+                    s = load_seq(p, b);
+                }
+                continue;
+            }
+            it = item_of(p, s, tile);
+            const int c = it.two ? p.c2 : p.c1;
+            // tile j is this CTA's where at + c0 + j * c lies in [begin, end)
+            const long long x0 = at + p.c0, x1 = x0 + static_cast<long long>(it.nt) * c;
+            auto first_from = [&](long long x) {        // (differences below x1 - x0 fit an int)
+                return x <= x0 ? 0 : x >= x1 ? it.nt : (static_cast<int>(x - x0) + c - 1) / c;
+            };
+            j0 = first_from(begin);
+            j1 = first_from(end);
+            cur_kvh = kvh;
+            cur_b = b;
+            at = x1;
+            ++tile;
+            if (j0 < j1) return true;
+        }
+    }
+    __device__ __forceinline__ int key0(int j) const { return it.base + j * 128; }
+    // a tile of cache keys that not every row of the item sees whole
+    __device__ __forceinline__ bool partial(int j) const {
+        return key0(j) < it.all_lo || key0(j) + 128 > it.all_hi;
+    }
+};
+
+__device__ __forceinline__ long long slot_row(const ChunkParams &p, int cta, int which) {
+    return (2LL * cta + which) * p.slot_rows;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------- kernel
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ ChunkParams p) {
+    using C = Cfg<D, Q8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *q_full = bars, *q_empty = bars + 1, *o_full = bars + 2, *o_empty = bars + 3, *drain = bars + 4;
+    uint64_t *k_full = bars + 5, *k_empty = k_full + C::NK, *v_full = k_empty + C::NK, *v_empty = v_full + C::NV;
+    uint64_t *v_fix = v_empty + C::NV, *s_full = v_fix + C::NV, *p_ready = s_full + 2;
+    uint32_t *s_poison = reinterpret_cast<uint32_t *>(smem + C::OFF_POISON);
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
+    int *s_parent = reinterpret_cast<int *>(smem + C::OFF_PARENT);
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 8);                       // one arrive per softmax warp
+        mbar_init(q_empty, 1);
+        mbar_init(o_full, 1);
+        mbar_init(o_empty, 8);
+        for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 4 : 1); mbar_init(k_empty + i, 1); }
+        for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 4 : 1); mbar_init(v_empty + i, 1); mbar_init(v_fix + i, 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(s_full + i, 1); mbar_init(p_ready + i, 4); }
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x < kPoisonRing * 4) s_poison[threadIdx.x] = 0;
+    if (warp == kWarpMma) {
+        tmem_alloc(s_tmem, 512);
+        tmem_relinquish();
+    }
+    // lengths, queries and the cache may come from the previous kernel
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.tree && blockIdx.x == 0 && warp == 0) check_ranges(p.q_start, p.B, p.N, p.status);
+    plan_start(p, reinterpret_cast<long long *>(smem + C::OFF_PLAN), s_start);
+    fence_proxy_async();                            // the plan's scratch becomes the K ring
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // Bounded waits; the first that gives up ends the others of the CTA soon.
+    auto give_up = [&]() {
+        *s_abort = 1;
+        raise_status(p.status, kStatusPipelineTimeout);
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const uint32_t a = smem_u32(bar);
+        if (mbar_test(a, parity & 1)) return true;
+        const long long t0 = clock64();
+        for (uint32_t i = 1;; ++i) {
+            if (mbar_try_wait(a, parity & 1)) return true;
+            if ((i & 63u) == 0) {
+                if (*s_abort) return false;
+                if (clock64() - t0 > kWaitLimitCycles) { give_up(); return false; }
+            }
+        }
+    };
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(bar, parity));
+    };
+
+    Walk w;
+    const int bs = p.cache.block_size;
+
+    if (warp == kWarpK || warp == kWarpV) {
+        // ------------------------------------------ TMA producers (bf16 cache)
+        regs_dec<C::REGS_OTHER>();
+        if constexpr (!Q8) {
+            const bool is_k = warp == kWarpK;
+            const int ns = is_k ? C::NK : C::NV;
+            uint8_t *ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+            if (lane == 0) tma_prefetch_desc(map);
+            const int nb = 128 / bs;
+            int st = 0, ph = 1, issued = 0;
+            bool ok = true;
+            w.start(p, s_start);
+            while (ok && w.next(p)) {
+                const int32_t *row = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
+                const int first = w.it.lo / bs, last = (w.it.hi - 1) / bs;
+                // blocks outside the item's keys are not looked up: their rows
+                // repeat a block inside (masked, and zeroed in V)
+                auto fetch = [&](int j) {
+                    return lane < nb && w.it.hi > 0 ? row[min(max(w.key0(j) / bs + lane, first), last)] : 0;
+                };
+                int id = fetch(w.j0);
+                for (int j = w.j0; j < w.j1; ++j) {
+                    if (!warp_wait(empty + st, ph)) { ok = false; break; }
+                    if (w.it.hi == 0) {             // nothing to read: a wholly masked tile
+                        if (lane == 0) mbar_arrive(full + st);
+                    } else {
+                        if (lane == 0) mbar_arrive_expect_tx(full + st, C::TILE);
+                        __syncwarp();
+                        if (lane < nb) {
+                            int n = id;
+                            if (n < 0 || n >= p.cache.num_blocks) {
+                                raise_status(p.status, kStatusBadBlock);
+                                n = 0;
+                            }
+                            const int y = (n * p.Hkv + w.cur_kvh) * bs;
+                            uint8_t *stage = ring + st * C::TILE + lane * bs * 128;
+#pragma unroll
+                            for (int h = 0; h < C::HALVES; ++h)
+                                tma_load_2d(stage + h * C::BOX, map, full + st, h * 64, y);
+                        }
+                    }
+                    if (j + 1 < w.j1) id = fetch(j + 1);
+                    ++issued;
+                    if (++st == ns) { st = 0; ph ^= 1; }
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && *s_abort)              // let the copies in flight land
+                for (int i = max(0, issued - ns); i < issued; ++i) mbar_wait(full + i % ns, (i / ns) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kWarpFix) {
+        // ------------------- partly visible V tiles of a bf16 cache, in place
+        // (every tile passes here, so that the phases of v_fix follow the ring)
+        regs_dec<C::REGS_OTHER>();
+        if constexpr (!Q8) {
+            int pos = 0;
+            bool ok = true;
+            w.start(p, s_start);
+            while (ok && w.next(p)) {
+                for (int j = w.j0; j < w.j1; ++j, ++pos) {
+                    const int st = pos % C::NV;
+                    if (!warp_wait(v_full + st, pos / C::NV)) { ok = false; break; }
+                    if (!w.partial(j)) {
+                        if (lane == 0) mbar_arrive(v_fix + st);
+                        continue;
+                    }
+                    uint8_t *sv = smem + C::OFF_V + st * C::TILE;
+                    const int a = w.it.lo - w.key0(j), z = w.it.hi - w.key0(j);   // live rows [a, z)
+                    // a row per lane, four rounds; all values in 16-byte pieces
+                    for (int g = 0; g < 4; ++g) {
+                        const int r = g * 32 + lane;
+                        uint8_t *rp = sv + r * 128;
+                        uint32_t big = 0;
+                        const bool live = r >= a && r < z;
+                        if (live) {
+#pragma unroll
+                            for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 u = *reinterpret_cast<const uint4 *>(rp + h * C::BOX + ((c ^ (r & 7)) << 4));
+                                    big = __vmaxu2(big, u.x & 0x7fff7fffu);
+                                    big = __vmaxu2(big, u.y & 0x7fff7fffu);
+                                    big = __vmaxu2(big, u.z & 0x7fff7fffu);
+                                    big = __vmaxu2(big, u.w & 0x7fff7fffu);
+                                }
+                        }
+                        const bool inf = max(big & 0xffffu, big >> 16) >= 0x7f80u;
+                        if (!live || inf) {
+#pragma unroll
+                            for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(rp + h * C::BOX + ((c ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        const uint32_t word = __ballot_sync(0xffffffffu, inf);
+                        if (lane == 0) s_poison[(pos % kPoisonRing) * 4 + g] = word;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_fix + st);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // -------------------------------------------------------------- MMA
+        regs_dec<C::REGS_OTHER>();
+        const uint64_t qdesc = smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+        const uint64_t kdesc = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+        const uint64_t vdesc = smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
+        int kst = 0, kph = 0, vst = 0, vph = 0;     // ring places of the next K / V tile
+        int cnt0 = 0, cnt1 = 0;                     // softmax steps of each group so far
+        int items = 0;
+        bool ok = true;
+        w.start(p, s_start);
+        while (ok && w.next(p)) {
+            const int two = w.it.two, n_steps = (w.j1 - w.j0) << two;
+            int kw = 0;                             // K tiles of the item waited for
+            auto qk = [&](int s) -> bool {          // scores of step s
+                const int g = s & 1, tile = s >> two;
+                if (tile >= kw) {
+                    if (!warp_wait(k_full + kst, kph)) return false;
+                    ++kw;
+                    tc_fence_after();
+                }
+                const uint64_t kd = kdesc + ((kst * C::TILE) >> 4);
+                const uint64_t qd = qdesc + (two ? (g * C::TILE) >> 4 : 0);
+                const bool done = !two || g == 1;   // the tile's last use
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + C::COL_S + g * 128, qd + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(s_full + g);
+                    if (done) mma_commit(k_empty + kst);
+                    if (s == n_steps - 1) mma_commit(q_empty);
+                }
+                if (done && ++kst == C::NK) { kst = 0; kph ^= 1; }
+                return true;
+            };
+            ok = warp_wait(q_full, items);
+            tc_fence_after();
+            for (int s = 0; ok && s < min(2, n_steps); ++s) ok = qk(s);
+            if (ok) ok = warp_wait(o_empty, items + 1);
+            for (int s = 0; ok && s < n_steps; ++s) {
+                const int g = s & 1;
+                if (!two || g == 0) {
+                    ok = warp_wait((Q8 ? v_full : v_fix) + vst, vph);
+                }
+                if (ok) ok = warp_wait(p_ready + g, g ? cnt1 : cnt0);
+                if (!ok) break;
+                if (g) ++cnt1; else ++cnt0;
+                tc_fence_after();
+                const uint64_t vd = vdesc + ((vst * C::TILE) >> 4);
+                const bool done = !two || g == 1;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + C::COL_O + g * D, tmem + C::COL_S + g * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4),
+                               C::IDESC_PV, (s > 1 || kk > 0) ? 1u : 0u);
+                    if (done) mma_commit(v_empty + vst);
+                    if (s == n_steps - 1) mma_commit(o_full);
+                }
+                if (done && ++vst == C::NV) { vst = 0; vph ^= 1; }
+                if (s + 2 < n_steps) ok = qk(s + 2);
+            }
+            ++items;
+        }
+        if (elect_one()) mma_commit(drain);         // all MMAs issued are done before TMEM is freed
+        warp_wait(drain, 0);
+    } else if (warp >= kWarpLoad) {
+        // --------------------------------------------- loaders (e4m3 cache)
+        if constexpr (Q8) {
+            regs_dec<C::REGS_LOAD>();
+            constexpr int LPR = D / 16;             // lanes per cache row (16 codes each)
+            constexpr int RPR = 128 / LPR;          // rows a round of the four warps covers: 16 (D = 128) or 32
+            constexpr int ROUNDS = 128 / RPR;
+            const int lw = warp - kWarpLoad;
+            const int row_in = lw * (32 / LPR) + lane / LPR, c = lane % LPR;
+            int kst = 0, kph = 1, vst = 0, vph = 1, pos = 0;
+            bool ok = true;
+            struct Regs { uint4 u[ROUNDS]; uint32_t e[(ROUNDS + 3) / 4]; };
+            const int nb = 128 / bs;
+            w.start(p, s_start);
+            while (ok && w.next(p)) {
+                const int32_t *trow = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
+                auto cached = [&](int j) { return j < w.it.cache_tiles; };
+                // blocks of a tile, lane i holding the i-th (outside the item's
+                // keys: one inside, whose rows are not read)
+                const int first_b = w.it.lo / bs, last_b = max(w.it.hi - 1, 0) / bs;
+                auto fetch = [&](int j) {
+                    if (lane >= nb || w.it.hi == 0 || !cached(j)) return 0;
+                    return static_cast<int>(trow[min(max(w.key0(j) / bs + lane, first_b), last_b)]);
+                };
+                auto checked = [&](int n) {
+                    if (n < 0 || n >= p.cache.num_blocks) {
+                        raise_status(p.status, kStatusBadBlock);
+                        n = 0;
+                    }
+                    return n;
+                };
+                // codes and scale bytes of one tile into registers; rows outside
+                // [lo, hi) are not read
+                auto load = [&](int j, int ids, bool is_v, Regs &r) {
+                    const uint8_t *src = static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k);
+                    const uint8_t *sc = is_v ? p.cache.v_scale : p.cache.k_scale;
+#pragma unroll
+                    for (int i = 0; i < (ROUNDS + 3) / 4; ++i) r.e[i] = 0;
+#pragma unroll
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        const int at = i * RPR + row_in, key = w.key0(j) + at;
+                        const int n = __shfl_sync(0xffffffffu, ids, at / bs);
+                        r.u[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (key >= w.it.lo && key < w.it.hi) {
+                            const size_t row = (static_cast<size_t>(n) * p.Hkv + w.cur_kvh) * bs + at % bs;
+                            r.u[i] = *reinterpret_cast<const uint4 *>(src + row * D + c * 16);
+                            r.e[i / 4] |= static_cast<uint32_t>(sc[row]) << (8 * (i % 4));
+                        }
+                    }
+                };
+                // bf16 rows of a swizzled tile from codes
+                auto store = [&](uint8_t *tile, const Regs &r, bool is_v) {
+#pragma unroll
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        const int key = i * RPR + row_in;
+                        int e = (r.e[i / 4] >> (8 * (i % 4))) & 255;
+                        uint4 u = r.u[i];
+                        if (is_v && e == kScaleNan) { u = make_uint4(0u, 0u, 0u, 0u); e = kScaleMin; }
+                        const uint32_t mult = e4m3_mult(e);
+                        const uint2 a = dequant_e4m3x4(u.x, mult), b = dequant_e4m3x4(u.y, mult);
+                        const uint2 d = dequant_e4m3x4(u.z, mult), f = dequant_e4m3x4(u.w, mult);
+                        uint4 x = make_uint4(a.x, a.y, b.x, b.y), y = make_uint4(d.x, d.y, f.x, f.y);
+                        // 16-byte pieces 2c and 2c+1 of the row; lanes of the two 64-column
+                        // halves write them in opposite order, so that eight lanes of a row
+                        // meet eight different bank groups
+                        const int q0 = 2 * c, half = q0 >> 3;
+                        int first = q0 & 7, second = first + 1;
+                        if (half) {
+                            const uint4 t = x; x = y; y = t;
+                            const int o = first; first = second; second = o;
+                        }
+                        uint8_t *rp = tile + half * C::BOX + key * 128;
+                        *reinterpret_cast<uint4 *>(rp + ((first ^ (key & 7)) << 4)) = x;
+                        *reinterpret_cast<uint4 *>(rp + ((second ^ (key & 7)) << 4)) = y;
+                    }
+                };
+                // scale byte of V row lw * 32 + lane of cache tile j: rows held as NaN
+                // are told to the softmax groups with the tile's K
+                auto v_byte = [&](int j, int ids) {
+                    const int at = lw * 32 + lane, key = w.key0(j) + at;
+                    const int n = __shfl_sync(0xffffffffu, ids, at / bs);
+                    return key >= w.it.lo && key < w.it.hi
+                               ? static_cast<int>(p.cache.v_scale[(static_cast<size_t>(n) * p.Hkv + w.cur_kvh) * bs + at % bs])
+                               : 0;
+                };
+                // tree rows (bf16, contiguous): 16 lanes a row at D = 128, 8 at D = 64
+                auto tree_tile = [&](int j, const __nv_bfloat16 *src, uint8_t *tile, bool is_v, int at) {
+                    constexpr int L2 = D / 8, R2 = 32 / L2;      // lanes per row, rows per warp and round
+                    const int cc = lane % L2, key_first = (j - w.it.cache_tiles) * 128;
+                    uint32_t word = 0;
+                    for (int i = 0; i < 32 / R2; ++i) {
+                        const int rr = lw * 32 + i * R2 + lane / L2;   // row of the tile; a warp has 32 of them
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (key_first + rr < p.N)
+                            u = *reinterpret_cast<const uint4 *>(
+                                src + ((static_cast<size_t>(w.cur_b) * p.Hkv + w.cur_kvh) * p.N + key_first + rr) * D + cc * 8);
+                        if (is_v) {
+                            uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                                  __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+                            const uint32_t lanes = __ballot_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
+                            const uint32_t mine = (lanes >> (lane / L2 * L2)) & ((1ull << L2) - 1);
+                            if (mine) u = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int g = 0; g < R2; ++g)
+                                if ((lanes >> (g * L2)) & ((1ull << L2) - 1)) word |= 1u << (i * R2 + g);
+                        }
+                        if (tile)
+                            *reinterpret_cast<uint4 *>(tile + (cc >> 3) * C::BOX + rr * 128 + (((cc & 7) ^ (rr & 7)) << 4)) = u;
+                    }
+                    if (at >= 0 && lane == 0) s_poison[at * 4 + lw] = word;
+                };
+                auto publish = [&](uint64_t *full) {
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
+                };
+                // fill order K0 K1 V0 K2 V1 ...: the unit after next is on its way
+                // from memory while this one is converted
+                Regs rk, rv;
+                int id_k = checked(fetch(w.j0)), id_v = id_k, id_next = fetch(w.j0 + 1), vb = 0;
+                if (cached(w.j0)) {
+                    load(w.j0, id_k, false, rk);
+                    vb = v_byte(w.j0, id_k);
+                }
+                for (int j = w.j0; j <= w.j1; ++j) {
+                    if (j > w.j0 && cached(j - 1)) load(j - 1, id_v, true, rv);
+                    if (j < w.j1) {
+                        if (!warp_wait(k_empty + kst, kph)) { ok = false; break; }
+                        uint8_t *tile = smem + C::OFF_K + kst * C::TILE;
+                        const int at = pos % kPoisonRing;
+                        if (cached(j)) {
+                            const uint32_t word = __ballot_sync(0xffffffffu, vb == kScaleNan);
+                            if (lane == 0) s_poison[at * 4 + lw] = word;
+                            store(tile, rk, false);
+                        } else {
+                            tree_tile(j, p.k_tree, tile, false, -1);
+                            tree_tile(j, p.v_tree, nullptr, true, at);
+                        }
+                        publish(k_full + kst);
+                        if (++kst == C::NK) { kst = 0; kph ^= 1; }
+                        ++pos;
+                        id_v = id_k;
+                        if (j + 1 < w.j1 && cached(j + 1)) {
+                            id_k = checked(id_next);
+                            id_next = fetch(j + 2);
+                            load(j + 1, id_k, false, rk);
+                            vb = v_byte(j + 1, id_k);
+                        }
+                    }
+                    if (j > w.j0) {
+                        if (!warp_wait(v_empty + vst, vph)) { ok = false; break; }
+                        uint8_t *tile = smem + C::OFF_V + vst * C::TILE;
+                        if (cached(j - 1)) store(tile, rv, true);
+                        else tree_tile(j - 1, p.v_tree, tile, true, -1);
+                        publish(v_full + vst);
+                        if (++vst == C::NV) { vst = 0; vph ^= 1; }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        regs_inc<C::REGS_SOFTMAX>();
+        const int grp = (warp - kWarpSoftmax) >> 2, wq = warp & 3;
+        const int r = wq * 32 + lane;                       // row of the tile = TMEM lane
+        const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t t_s = tmem + lane_addr + C::COL_S + grp * 128;
+        const uint32_t t_o = tmem + lane_addr + C::COL_O;
+        const float c2 = p.scale_log2, nan = __int_as_float(0x7fc00000);
+        int cnt = 0, items = 0, pos = 0;                    // steps of this group, items, key tiles so far
+        bool ok = true;
+        w.start(p, s_start);
+        // both partial slots' headers are written by every launch
+        int head_first = -1, head_last = -1;
+        while (w.next(p)) {
+            const int two = w.it.two;
+            const int row = two ? grp * 128 + r : r;        // row of the item
+            const bool valid = row < w.it.rows;
+            const bool warp_active = (two ? grp * 128 : 0) + wq * 32 < w.it.rows;
+            const int pr = w.it.r0 + (valid ? row : 0);     // packed row
+            int t = 0, g = 0;
+            size_t orow;
+            const __nv_bfloat16 *qp;
+            if (p.tree) {
+                t = pr % p.N;
+                orow = (static_cast<size_t>(w.cur_b) * p.Hq + static_cast<size_t>(w.cur_kvh) * p.G) * p.N + pr;
+                qp = p.q + orow * D;
+            } else {
+                t = pr / p.G;
+                g = pr - t * p.G;
+                const int h = w.cur_kvh * p.G + g;
+                orow = static_cast<size_t>(w.s.s0 + t) * p.Hq + h;
+                qp = p.q + (w.s.s0 + t) * p.q_stride + static_cast<size_t>(h) * D;
+            }
+            if (w.s.bad && threadIdx.x == kWarpSoftmax * 32) raise_status(p.status, kStatusPrefixLenRange);
+            bool row_nan = w.s.bad;
+            // ---- Q into shared memory (one row tile: each group half of the columns)
+            {
+                const int ch0 = two ? 0 : grp * (D / 16), nch = two ? D / 8 : D / 16;
+                uint4 qv[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    if (i < nch) qv[i] = valid ? reinterpret_cast<const uint4 *>(qp)[ch0 + i] : make_uint4(0u, 0u, 0u, 0u);
+                if (ok) ok = warp_wait(q_empty, items + 1);
+                uint8_t *qs = smem + C::OFF_Q + (two ? grp * C::TILE : 0) + r * 128;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    if (i < nch) {
+                        const int ch = ch0 + i;
+                        *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::BOX + (((ch & 7) ^ (r & 7)) << 4)) = qv[i];
+                    }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            bool tree_bad = false;
+            if (w.j1 > w.it.cache_tiles) {                  // this CTA has keys of the tree
+                const int i = (warp - kWarpSoftmax) * 32 + lane;
+                bar_sync(1, 256);                           // the last item's walks are over
+                bool bad = false;
+                if (i < p.N) {
+                    const int up = p.parent[static_cast<size_t>(w.cur_b) * p.N + i];
+                    bad = up < -1 || up >= i;
+                    s_parent[i] = up;
+                }
+                __syncwarp();
+                tree_bad = bar_or(1, 256, bad);
+                if (tree_bad && i == 0) raise_status(p.status, kStatusBadParent);
+                row_nan |= tree_bad;
+            }
+            const int row_hi = p.tree ? w.it.hi : (w.s.bad ? 0 : w.s.L + t + 1);
+            const int row_lo = p.window > 0 ? max(0, row_hi - p.window) : 0;
+
+            float m_run = -INFINITY;
+            uint64_t l2 = 0;
+            const int n_tiles = w.j1 - w.j0;
+            const int step = two ? 1 : 2;
+            for (int jj = two ? 0 : grp; jj < n_tiles; jj += step) {
+                const int j = w.j0 + jj;
+                if (ok) ok = warp_wait(s_full + grp, cnt);
+                ++cnt;
+                tc_fence_after();
+                if (ok && warp_active) {
+                    uint32_t r0[32], r1[32], r2[32], r3[32];
+                    tmem_ld32(t_s + 0, r0);
+                    tmem_ld32(t_s + 32, r1);
+                    tmem_ld32(t_s + 64, r2);
+                    tmem_ld32(t_s + 96, r3);
+                    const bool of_tree = j >= w.it.cache_tiles;
+                    uint4 bad_v = make_uint4(0u, 0u, 0u, 0u);
+                    if (Q8) bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
+                    tmem_wait_ld();
+                    if (of_tree || w.partial(j)) {
+                        uint32_t see[4];
+                        if (of_tree) {
+                            const int first = (j - w.it.cache_tiles) * 128;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) see[i] = 0;
+                            for (int node = tree_bad ? -1 : t; node >= 0; node = s_parent[node]) {   // (parents lie below their nodes)
+                                const int d = node - first;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) see[i] |= (d >> 5) == i ? 1u << (d & 31) : 0u;
+                            }
+                        } else {
+                            const int a = row_lo - w.key0(j), z = row_hi - w.key0(j);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) see[i] = bit_range(a - 32 * i, z - 32 * i);
+                            if (!Q8) {
+                                // the fixer's word on this tile
+                                ok = warp_wait(v_fix + (pos + jj) % C::NV, (pos + jj) / C::NV);
+                                bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
+                            }
+                        }
+                        const uint32_t ninf = __float_as_uint(-INFINITY);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            r0[i] = (see[0] >> i) & 1u ? r0[i] : ninf;
+                            r1[i] = (see[1] >> i) & 1u ? r1[i] : ninf;
+                            r2[i] = (see[2] >> i) & 1u ? r2[i] : ninf;
+                            r3[i] = (see[3] >> i) & 1u ? r3[i] : ninf;
+                        }
+                        __syncwarp();
+                        if ((see[0] & bad_v.x) | (see[1] & bad_v.y) | (see[2] & bad_v.z) | (see[3] & bad_v.w)) row_nan = true;
+                    } else if (Q8) {
+                        if (bad_v.x | bad_v.y | bad_v.z | bad_v.w) row_nan = true;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        m4[0] = max3(m4[0], __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
+                        m4[1] = max3(m4[1], __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
+                        m4[2] = max3(m4[2], __uint_as_float(r2[i]), __uint_as_float(r2[i + 1]));
+                        m4[3] = max3(m4[3], __uint_as_float(r3[i]), __uint_as_float(r3[i + 1]));
+                    }
+                    const float m_tile = max3(max3(m4[0], m4[1], m4[2]), m4[3], -INFINITY) * c2;
+                    if (m_tile != m_tile) row_nan = true;
+                    const float m_new = fmaxf(m_run, m_tile);
+                    bool resc = false;
+                    float alpha = 1.f;
+                    if (m_new > m_run + 8.f) {
+                        alpha = ex2(m_run - m_new);         // 0 on the first tile with a visible key
+                        l2 = fma2(l2, f2(alpha, alpha), 0ull);
+                        resc = jj >= step;                  // (O holds nothing before the group's second tile)
+                        m_run = m_new;
+                    }
+                    const float mu = m_run == -INFINITY ? 0.f : m_run;
+                    const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
+                    auto exps = [&](const uint32_t (&sc)[32], int col) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t x2 = fma2(f2(__uint_as_float(sc[2 * k]), __uint_as_float(sc[2 * k + 1])), cc, nm);
+                            float2 e;
+                            constexpr int kEvery = HTA_EXP2_POLY_EVERY;
+                            if (kEvery > 0 && k % kEvery == kEvery - 1) {
+                                e = exp2_poly2(x2);
+                            } else {
+                                const float2 x = unf2(x2);
+                                e = make_float2(ex2(x.x), ex2(x.y));
+                            }
+                            pk[k] = pack_bf16x2(e.x, e.y);
+                            l2 = add2(l2, f2(e.x, e.y));
+                        }
+                        tmem_st16(t_s + col, pk);
+                    };
+                    exps(r0, 0);
+                    exps(r1, 16);
+                    exps(r2, 32);
+                    exps(r3, 48);
+                    if (__any_sync(0xffffffffu, resc)) {
+                        // this tile's scores were committed after P*V of the group's previous
+                        // tile, so O[grp] is complete, and P*V of this tile waits for this warp
+                        const float a = resc ? alpha : 1.f;
+#pragma unroll 1
+                        for (int col = 0; col < D; col += 32) {
+                            uint32_t ro[32];
+                            tmem_ld32(t_o + grp * D + col, ro);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) ro[i] = __float_as_uint(__uint_as_float(ro[i]) * a);
+                            tmem_st32(t_o + grp * D + col, ro);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + grp);
+            }
+
+            // ------------------------------------------------------ epilogue
+            if (ok) ok = warp_wait(o_full, items);
+            tc_fence_after();
+            const float2 lp = unf2(l2);
+            float l = m_run == -INFINITY ? 0.f : lp.x + lp.y, m = m_run;
+            float a0 = 1.f, a1 = 0.f;
+            bool has1 = false;
+            if (!two) {                                     // join the groups: key tiles 0, 2, .. and 1, 3, ..
+                float *xch = reinterpret_cast<float *>(smem + C::OFF_XCH);
+                xch[(grp * 2 + 0) * 128 + r] = m;
+                xch[(grp * 2 + 1) * 128 + r] = l;
+                row_nan = row_nan | (ok ? false : true);
+                // (row_nan of either group: through the sum)
+                if (row_nan) xch[(grp * 2 + 1) * 128 + r] = nan;
+                bar_sync(1, 256);
+                const float m0 = xch[r], m1 = xch[2 * 128 + r];
+                m = fmaxf(m0, m1);
+                a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+                a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                const float l0 = xch[128 + r], l1 = xch[3 * 128 + r];
+                l = a0 * l0 + a1 * l1;
+                row_nan = l0 != l0 || l1 != l1;
+                has1 = n_tiles > 1;
+                bar_sync(1, 256);                           // read before the next item's Q lands there
+            } else if (!ok) {
+                row_nan = true;
+            }
+            const bool whole = w.j0 == 0 && w.j1 == w.it.nt;
+            if (l != l) row_nan = true;
+            const float inv = row_nan ? nan : l > 0.f ? 1.f / l : 0.f;
+            const float lse = row_nan ? nan : l > 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
+            const int which = w.j0 > 0 ? 0 : 1;             // the CTA's first item, begun elsewhere, or its last
+            const long long prow = slot_row(p, blockIdx.x, which) + row;
+            const int col0 = two ? 0 : grp * (D / 2), col1 = two ? D : col0 + D / 2;
+            if (warp_active) {
+                const float f0 = a0 * inv, f1 = a1 * inv;
+                const uint32_t to0 = t_o + (two ? grp * D : 0), to1 = t_o + D;
+#pragma unroll 1
+                for (int col = col0; col < col1; col += 32) {
+                    uint32_t x0[32], x1[32];
+                    float y[32];
+                    tmem_ld32(to0 + col, x0);
+                    if (has1) tmem_ld32(to1 + col, x1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        y[i] = __uint_as_float(x0[i]) * f0;
+                        if (has1) y[i] = fmaf(__uint_as_float(x1[i]), f1, y[i]);
+                        if (l == 0.f && !row_nan) y[i] = 0.f;
+                    }
+                    if (valid && whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + col);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                                pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+                    } else if (valid) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.o_part + prow * D + col);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && (two || grp == 0)) {
+                    if (whole) p.lse[orow] = lse;
+                    else p.lse_part[prow] = lse;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty);
+            if (!whole && threadIdx.x == kWarpSoftmax * 32) {
+                PartHead hd;
+                hd.b = w.cur_b;
+                hd.kvh = w.cur_kvh;
+                hd.r0 = w.it.r0;
+                hd.rows = w.it.rows;
+                hd.s0 = w.s.s0;
+                hd.last = w.j1 == w.it.nt;
+                hd.pad0 = hd.pad1 = 0;
+                p.heads[2 * blockIdx.x + which] = hd;
+                if (which == 0) head_first = 1; else head_last = 1;
+            }
+            ++items;
+            pos += n_tiles;
+        }
+        if (threadIdx.x == kWarpSoftmax * 32) {
+            if (head_first < 0) p.heads[2 * blockIdx.x].rows = 0;
+            if (head_last < 0) p.heads[2 * blockIdx.x + 1].rows = 0;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------- merge
+// Rows of items that crossed CTA borders: the partials of an item are slot 1
+// of the CTA it begins in and slots 0 of the next ones.  One warp per row:
+//   out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M},  lse = M + ln(sum).
+template <int D>
+__global__ void __launch_bounds__(256)
+chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int DPL = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    const PartHead hd = p.heads[2 * cta + 1];
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (row >= hd.rows) return;
+    int n = 1;                                  // partials: CTAs cta .. cta + n - 1
+    if (!hd.last)
+        for (int c = cta + 1;; c += 32) {       // the first CTA whose segment is the item's last
+            const bool last = c + lane < p.grid ? p.heads[2 * (c + lane)].last != 0 || p.heads[2 * (c + lane)].rows == 0 : true;
+            const uint32_t m = __ballot_sync(0xffffffffu, last);
+            if (m) { n = c + __ffs(m) - 1 - cta + 1; break; }
+        }
+    n = min(n, p.grid - cta);
+    auto slot = [&](int i) { return slot_row(p, cta + i, i == 0 ? 1 : 0) + row; };
+    float mx = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < n; i += 32) {
+        const float v = p.lse_part[slot(i)];
+        bad |= v != v;
+        mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    bad = __any_sync(0xffffffffu, bad);
+    float acc[DPL], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float wgt = i0 + lane < n ? ex2((p.lse_part[slot(i0 + lane)] - mx) * kLog2e) : 0.f;
+        if (mx == -INFINITY) wgt = 0.f;
+        const int here = min(32, n - i0);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, wgt, i);
+            const float *src = p.o_part + slot(i0 + i) * D + lane * DPL;
+            float v[DPL];
+            if constexpr (DPL == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(src);
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(src);
+                v[0] = x.x; v[1] = x.y;
+            }
+            sum += wi;
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) acc[k] = wi > 0.f ? fmaf(wi, v[k], acc[k]) : acc[k];
+        }
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    const float inv = bad ? nan : sum > 0.f ? 1.f / sum : 0.f;
+    const float lse = bad ? nan : sum > 0.f ? mx + lg2(sum) * kLn2 : -INFINITY;
+    size_t orow;
+    const int pr = hd.r0 + row;
+    if (p.tree) {
+        orow = (static_cast<size_t>(hd.b) * p.Hq + static_cast<size_t>(hd.kvh) * p.G) * p.N + pr;
+    } else {
+        const int t = pr / p.G;
+        orow = static_cast<size_t>(hd.s0 + t) * p.Hq + hd.kvh * p.G + (pr - t * p.G);
+    }
+    __nv_bfloat16 *dst = p.out + orow * D + lane * DPL;
+    if constexpr (DPL == 4) {
+        uint2 pk;
+        pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+        *reinterpret_cast<uint2 *>(dst) = pk;
+    } else {
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    }
+    if (lane == 0) p.lse[orow] = lse;
+}
+
+namespace {
+
+template <int D, bool Q8>
+cudaError_t launch(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t stream) {
+    using C = Cfg<D, Q8>;
+    constexpr int kMaxDev = 64;
+    static bool attr_set[kMaxDev] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDev || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_ALLOC;
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8>, tm_k, tm_v, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(p.grid, (p.slot_rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkParams &p0, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                            cudaStream_t stream) {
+    ChunkParams p = p0;
+    p.c0 = 4;
+    p.c1 = 4;
+    p.c2 = 8;
+    p.min_share = 8;
+    const bool q8 = p.cache.k_scale != nullptr;
+    if (p.D == 128) return q8 ? launch<128, true>(p, tm_k, tm_v, stream) : launch<128, false>(p, tm_k, tm_v, stream);
+    return q8 ? launch<64, true>(p, tm_k, tm_v, stream) : launch<64, false>(p, tm_k, tm_v, stream);
+}
+
+}  // namespace hta
