@@ -433,7 +433,7 @@ LONGSPEC_HTA_API int longspec_hta_commit_paged(const longspec_hta_dims *dims, co
  * longspec_hta_cache: a paged cache as in longspec_hta_paged_kv, in bf16
  * (k_scale and v_scale null) or in e4m3 (both set, uint8
  * [num_blocks][Hkv][block_size]; k_cache and v_cache then hold e4m3 codes in
- * the same layout, 16-byte aligned).  A row x of D values is kept as D codes
+ * the same layout; scales 16-byte aligned too).  A row x of D values is kept as D codes
  * c and one byte e:
  *   x ~ c * 2^(e - 127), 2^(e - 127) the smallest power of two with
  *   max|x| <= 448 * 2^(e - 127), e clamped to [16, 134]

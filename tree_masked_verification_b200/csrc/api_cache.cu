@@ -30,6 +30,7 @@ int check_cache(const longspec_hta_cache *c, const longspec_hta_dims *d) {
     if (!aligned16(c->k_cache) || !aligned16(c->v_cache) || !aligned4(c->block_table))
         return LONGSPEC_HTA_ERR_MISALIGNED;
     if ((c->k_scale == nullptr) != (c->v_scale == nullptr)) return LONGSPEC_HTA_ERR_INVALID_OPTION;
+    if (!aligned16(c->k_scale) || !aligned16(c->v_scale)) return LONGSPEC_HTA_ERR_MISALIGNED;
     const int bs = c->block_size;
     if ((bs != 16 && bs != 32 && bs != 64 && bs != 128) || c->num_blocks < 1 || c->max_blocks < 1 ||
         1LL * c->max_blocks * bs < d->L_cap || 1LL * c->max_blocks * bs >= kIntLimit ||
@@ -102,17 +103,17 @@ SlotLayout slot_layout(long long packed_rows, int D, int grid) {
     return l;
 }
 
-// The bf16 cache as [num_blocks * Hkv * block_size][D] in boxes of one block's
-// rows by 64 columns, 128-byte swizzle.
-int cache_map(const void *base, const longspec_hta_cache *c, int Hkv, int D, CUtensorMap *out) {
+// Rows [rows][D] of bf16 in boxes of 64 columns, 128-byte swizzle, or of e4m3
+// codes in whole rows.
+int rows_map(const void *base, uint64_t rows, int D, int box_rows, bool q8, CUtensorMap *out) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return LONGSPEC_HTA_ERR_CUDA;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D),
-                                static_cast<cuuint64_t>(c->num_blocks) * Hkv * c->block_size};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(c->block_size)}, es[2] = {1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (q8 ? 1 : 2)};
+    const cuuint32_t box[2] = {q8 ? static_cast<cuuint32_t>(D) : 64u, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+    return fn(out, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
 }
@@ -134,12 +135,17 @@ int run_attention(hta::ChunkParams &p, const longspec_hta_dims *d, const longspe
     p.heads = reinterpret_cast<hta::PartHead *>(ws + l.heads_off);
     p.o_part = reinterpret_cast<float *>(ws + l.o_off);
     p.lse_part = reinterpret_cast<float *>(ws + l.lse_off);
-    CUtensorMap tk{}, tv{};
-    if (!cache->k_scale) {
-        HTA_TRY(cache_map(cache->k_cache, cache, d->Hkv, d->D, &tk));
-        HTA_TRY(cache_map(cache->v_cache, cache, d->Hkv, d->D, &tv));
+    CUtensorMap tm[4] = {};
+    const uint64_t cache_rows = 1ull * cache->num_blocks * d->Hkv * cache->block_size;
+    const bool q8 = cache->k_scale != nullptr;
+    HTA_TRY(rows_map(cache->k_cache, cache_rows, d->D, cache->block_size, q8, &tm[0]));
+    HTA_TRY(rows_map(cache->v_cache, cache_rows, d->D, cache->block_size, q8, &tm[1]));
+    if (p.tree_tiles) {
+        const uint64_t rows = 1ull * d->B * d->Hkv * d->T;
+        HTA_TRY(rows_map(p.k_tree, rows, d->D, 128, false, &tm[2]));
+        HTA_TRY(rows_map(p.v_tree, rows, d->D, 128, false, &tm[3]));
     }
-    return hta::launch_chunk_tc(p, tk, tv, stream) == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
+    return hta::launch_chunk_tc(p, tm, stream) == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA; }

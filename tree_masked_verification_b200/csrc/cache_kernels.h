@@ -77,7 +77,7 @@ cudaError_t launch_commit_q8(const CommitQ8Params &p, cudaStream_t stream);
 // Which rows a partial of chunk_tc_kernel belongs to.
 struct PartHead {
     int b, kvh, r0, rows;             // rows 0: the slot is empty
-    int s0, last, pad0, pad1;         // last: the item's last segment
+    int s0, n, pad0, pad1;            // n (slot 1): segments of the item
 };
 
 // Attention of query rows to a paged cache.  Two row layouts:
@@ -102,14 +102,17 @@ struct ChunkParams {
     // schedule and partials (chunk_tc.cu): grid CTAs, two slots of slot_rows
     // rows each
     int grid, slot_rows;
+    uint32_t g_mul;                   // division by G (div_g)
+    int g_shift;
     int c0, c1, c2, min_share;        // units of work: an item, a key tile of one / two row tiles; least share of a CTA
     PartHead *heads;                  // [2 * grid]
     float *o_part, *lse_part;         // [2 * grid][slot_rows][D], [2 * grid][slot_rows]
 };
-// tm_k / tm_v: the caches as [num_blocks*Hkv*block_size][D], box 64 x
-// block_size, 128B swizzle (bf16 caches; not used for e4m3 ones)
-cudaError_t launch_chunk_tc(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                            cudaStream_t stream);
+// tm: K and V cache as [num_blocks*Hkv*block_size][D], bf16 in boxes of 64
+// columns by block_size rows with 128B swizzle, e4m3 in whole rows without;
+// K and V of the tree as [B*Hkv*N][D], box 64 x 128, 128B swizzle (not used
+// without tree tiles)
+cudaError_t launch_chunk_tc(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream);
 
 // -------------------------------------------------------------- device parts
 // The sequence of token i: the largest b with q_start[b] <= i, run by a whole

@@ -20,12 +20,16 @@
 // that crosses a border leaves normalised fp32 partials and their lse, at
 // most two per CTA (its first and its last item), which merge_kernel joins.
 //
-// Warps: 0 TMA producer of K, 1 MMA issuer, 2 TMA producer of V (bf16
-// caches), 3 fixer of partly visible V tiles, 4-7 and 8-11 two softmax groups
-// (one row per thread), 12-15 (e4m3 caches) loaders, which read codes into
-// registers one tile ahead, scale them exactly to bf16 and write the
-// swizzled tiles the MMAs read.  With two row tiles group g owns tile g and
-// runs every key tile; with one, group g runs the key tiles j = g mod 2 into
+// Warps: 0 TMA producer of K, 1 MMA issuer, 2 TMA producer of V, 3 fixer of
+// partly visible V tiles (bf16 caches), 4-7 and 8-11 two softmax groups (one
+// row per thread), 12-19 loaders (e4m3 caches).  TMA leaves a tile's codes in
+// the upper half of its stage; the loaders read them into registers and
+// write the whole stage over as the swizzled bf16 tile the MMAs read (an
+// exact product, see dequant_e4m3x4), so that codes need no buffers of their
+// own and the rings prefetch as deep as for bf16.  (Loads straight into
+// registers, one tile ahead, took 5 us a tile: a warp's waits on them cover
+// younger loads too, so that each tile waited for the next one's.)  With two
+// row tiles group g owns tile g and runs every key tile; with one, group g runs the key tiles j = g mod 2 into
 // an accumulator of its own and the two are merged at the end (the lse merge
 // of two key ranges).  Steps s of an item: group s & 1, key tile
 // s >> (two row tiles); MMA order QK_0 QK_1 [PV_0 QK_2] [PV_1 QK_3] ...
@@ -49,6 +53,7 @@ namespace {
 
 constexpr int kItemRows = 256;
 constexpr int kPoisonRing = 8;
+constexpr int kPlanUnits = 2048;
 
 template <int D, bool Q8>
 struct Cfg {
@@ -57,26 +62,31 @@ struct Cfg {
     static constexpr int HALVES = D / 64;                   // 64-column swizzle boxes
     static constexpr int BOX = 128 * 64 * 2;
     static constexpr int TILE = 128 * D * 2;
+    static constexpr int RAW = 128 * D;                     // a tile's codes, in the upper half of its stage
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = 2 * TILE;
     static constexpr int OFF_V = OFF_K + NK * TILE;
     static constexpr int OFF_BAR = OFF_V + NV * TILE;
-    // q_full, q_empty, o_full, o_empty, drain, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], v_fix[NV],
-    // s_full[2], p_ready[2]
-    static constexpr int NUM_BARS = 5 + 2 * NK + 3 * NV + 4;
+    // q_full, q_empty, o_full, o_empty, drain, k_full[NK], k_empty[NK], k_raw[NK], v_full[NV], v_empty[NV],
+    // v_raw[NV], s_full[2], p_ready[2].  x_raw: a tile as TMA left it; x_full: ready for the MMAs
+    static constexpr int NUM_BARS = 5 + 3 * NK + 3 * NV + 4;
     static constexpr int OFF_POISON = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // [kPoisonRing][4] words
-    static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort, walk start (b, kvh, tile), at, end
-    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // int32 [kTMax] (trees)
-    static constexpr int SMEM = OFF_PARENT + kTMax * 4;
+    static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort; Start
+    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // int16 [kTMax] (trees)
+    static constexpr int OFF_SCALE = OFF_PARENT + kTMax * 2;         // per K stage: scale bytes of K and of V
+    static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 : 0); // walks of the softmax groups and the loaders
+    static constexpr int WALK_BYTES = 160;
+    static constexpr int SMEM = OFF_WALK + 2 * WALK_BYTES;
     static constexpr int SMEM_ALLOC = SMEM + 1024;          // slack to align the base to 1024
     static constexpr int OFF_XCH = TILE;                    // [2][2][128] floats, in the unused second Q tile
-    static constexpr int OFF_PLAN = OFF_K;                  // int64 per 32 sequences, before the first copy
-    static constexpr int THREADS = Q8 ? 512 : 384;
-    // registers per thread: launch budget 65536 / THREADS (a multiple of 8)
-    static constexpr int REGS_SOFTMAX = Q8 ? 176 : 224;
-    static constexpr int REGS_LOAD = 96;
+    static constexpr int OFF_PLAN = OFF_K;                  // int64 [kPlanUnits], before the first copy
+    static constexpr int THREADS = Q8 ? 640 : 384;
+    // registers per thread; the launch allots LAUNCH_REGS to each
+    static constexpr int LAUNCH_REGS = Q8 ? 96 : 168;
+    static constexpr int REGS_SOFTMAX = Q8 ? 152 : 224;
+    static constexpr int REGS_LOAD = 56;
     static constexpr int REGS_OTHER = Q8 ? 64 : 56;
-    static_assert(256 * REGS_SOFTMAX + (Q8 ? 128 * REGS_LOAD : 0) + 128 * REGS_OTHER <= THREADS * (Q8 ? 128 : 168),
+    static_assert(256 * REGS_SOFTMAX + (Q8 ? 256 * REGS_LOAD : 0) + 128 * REGS_OTHER <= THREADS * LAUNCH_REGS,
                   "register split must fit the launch allocation");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false);
@@ -161,6 +171,13 @@ __device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
     return o;
 }
 
+// `bytes` contiguous bytes to shared memory (both ends 16-byte aligned, bytes a
+// multiple of 16), counted on `bar`
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, int bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
 // bits [lo, hi) of a 32-bit word (lo, hi any integers)
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     const int h = min(max(hi, 0), 32), l = min(max(lo, 0), 32);
@@ -193,6 +210,11 @@ __device__ __forceinline__ Seq load_seq(const ChunkParams &p, int b) {
     return s;
 }
 
+// x / G for 0 <= x < 2^31 (g_mul = floor(2^(31 + g_shift) / G) + 1 with 2^(g_shift - 1) < G <= 2^g_shift)
+__device__ __forceinline__ int div_g(const ChunkParams &p, int x) {
+    return p.G == 1 ? x : static_cast<int>(__umulhi(2u * static_cast<uint32_t>(x), p.g_mul) >> p.g_shift);
+}
+
 struct Item {
     int r0, rows;                   // packed rows [r0, r0 + rows)
     int two;                        // more than one 128-row tile
@@ -212,7 +234,7 @@ __device__ __forceinline__ Item item_of(const ChunkParams &p, const Seq &s, int 
     } else if (p.tree) {
         it.hi = it.all_hi = s.L;
     } else {
-        const int t0 = it.r0 / p.G, t1 = (it.r0 + it.rows - 1) / p.G;
+        const int t0 = div_g(p, it.r0), t1 = div_g(p, it.r0 + it.rows - 1);
         it.all_hi = s.L + t0 + 1;
         it.hi = s.L + t1 + 1;
         if (p.window > 0) {
@@ -220,7 +242,7 @@ __device__ __forceinline__ Item item_of(const ChunkParams &p, const Seq &s, int 
             it.all_lo = max(0, s.L + t1 - p.window + 1);
         }
     }
-    it.base = it.lo / p.cache.block_size * p.cache.block_size;
+    it.base = it.lo & ~(p.cache.block_size - 1);
     it.cache_tiles = (it.hi - it.base + 127) / 128;
     it.nt = it.cache_tiles + p.tree_tiles;
     if (it.nt == 0) it.nt = it.cache_tiles = 1;        // no key at all: one tile, wholly masked
@@ -231,31 +253,11 @@ __device__ __forceinline__ int item_cost(const ChunkParams &p, const Item &it) {
     return p.c0 + it.nt * (it.two ? p.c2 : p.c1);
 }
 
-// cost of the sequence of each lane (lanes without one: n = 0), for one KV head
-__device__ __forceinline__ long long seq_costs(const ChunkParams &p, const Seq &s) {
-    const int lane = threadIdx.x & 31;
-    long long cost = 0;
-    const bool big = s.tiles > 2;
-    if (!big)
-        for (int i = 0; i < s.tiles; ++i) cost += item_cost(p, item_of(p, s, i));
-    for (uint32_t m = __ballot_sync(0xffffffffu, big); m; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        Seq o;
-        o.s0 = 0;
-        o.n = 0;
-        o.L = __shfl_sync(0xffffffffu, s.L, src);
-        o.rows = __shfl_sync(0xffffffffu, s.rows, src);
-        o.tiles = __shfl_sync(0xffffffffu, s.tiles, src);
-        o.bad = __shfl_sync(0xffffffffu, s.bad ? 1 : 0, src) != 0;
-        long long c = 0;
-        for (int i = lane; i < o.tiles; i += 32) c += item_cost(p, item_of(p, o, i));
+__device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) c += __shfl_xor_sync(0xffffffffu, c, k);
-        if (lane == src) cost = c;
-    }
-    return cost;
+    for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    return v;
 }
-
 __device__ __forceinline__ long long scan_add(long long v) {     // inclusive, over the warp
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -266,77 +268,80 @@ __device__ __forceinline__ long long scan_add(long long v) {     // inclusive, o
     return v;
 }
 
+// cost of one KV head's items of a sequence, `first` by `step` of them
+__device__ __forceinline__ long long seq_cost(const ChunkParams &p, const Seq &s, int first, int step) {
+    long long cost = 0;
+    for (int i = first; i < s.tiles; i += step) cost += item_cost(p, item_of(p, s, i));
+    return cost;
+}
+
 struct Start {
     int b, kvh, tile, pad;
     long long at, begin, end;       // units: start of that item, this CTA's range
 };
 
-// Where this CTA's range of the work begins (the whole CTA calls; `plan` is
-// shared scratch of one int64 per 32 sequences).
+// The share of the work of each CTA, and where this CTA's begins (the whole
+// CTA calls).  `plan` (shared scratch) takes the cost of each sequence, or of
+// each 32 in batches of more than kPlanUnits: of long sequences a warp sums
+// one's items, of short ones a thread.
 __device__ void plan_start(const ChunkParams &p, long long *plan, Start *out) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int groups = (p.B + 31) / 32;
-    auto lane_seq = [&](int g) {
-        Seq s = {};
-        if (g * 32 + lane < p.B) s = load_seq(p, g * 32 + lane);
-        return s;
-    };
-    for (int g = warp; g < groups; g += warps) {
-        const long long c = scan_add(seq_costs(p, lane_seq(g)));
-        if (lane == 31) plan[g] = c;
+    const int per = p.B <= kPlanUnits ? 1 : 32, units = (p.B + per - 1) / per;
+    if (per == 32) {
+        for (int u = warp; u < units; u += warps) {
+            const int b = u * 32 + lane;
+            const long long c = warp_sum(b < p.B ? seq_cost(p, load_seq(p, b), 0, 1) : 0);
+            if (lane == 0) plan[u] = c;
+        }
+    } else if (static_cast<long long>(p.N) * p.G > 512LL * (p.tree ? 1 : p.B)) {
+        for (int b = warp; b < p.B; b += warps) {
+            const long long c = warp_sum(seq_cost(p, load_seq(p, b), lane, 32));
+            if (lane == 0) plan[b] = c;
+        }
+    } else {
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) plan[b] = seq_cost(p, load_seq(p, b), 0, 1);
     }
     __syncthreads();
     if (warp == 0) {
         long long total = 0;
-        for (int g = lane; g < groups; g += 32) total += plan[g];
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
-        const long long work = total * p.Hkv;
-        const long long share = max((work + gridDim.x - 1) / gridDim.x, static_cast<long long>(p.min_share));
+        for (int u = lane; u < units; u += 32) total += plan[u];
+        const long long work = warp_sum(total) * p.Hkv;
+        // (every CTA computes the same share; grid * share >= work)
+        const long long share = max(static_cast<long long>(static_cast<double>(work) / gridDim.x) + 1,
+                                    static_cast<long long>(p.min_share));
         const long long begin = share * blockIdx.x, end = min(work, begin + share);
         Start st = {p.B, 0, 0, 0, 0, begin, end};
         if (begin < work) {
-            long long before = 0;                       // of the KV-head-0 axis
-            int g = 0;
-            for (;; g += 32) {
-                const long long c = g + lane < groups ? plan[g + lane] : 0;
+            // the unit of sequences, the sequence, the KV head and the item that hold `begin`;
+            // `before`: the work before it
+            long long before = 0;
+            auto find = [&](long long c, int &k) {      // c: the lanes' costs (of all KV heads)
                 const long long cum = before + scan_add(c);
-                const uint32_t past = __ballot_sync(0xffffffffu, cum * p.Hkv > begin);
-                if (past) {
-                    const int k = __ffs(past) - 1;
-                    before = __shfl_sync(0xffffffffu, cum - c, k);
-                    g += k;
-                    break;
-                }
-                before = __shfl_sync(0xffffffffu, cum, 31);
+                const uint32_t past = __ballot_sync(0xffffffffu, cum > begin);
+                k = past ? __ffs(past) - 1 : 31;
+                before = __shfl_sync(0xffffffffu, past ? cum - c : cum, k);
+                return past != 0;
+            };
+            int k = 0, u = 0;
+            while (!find(u + lane < units ? plan[u + lane] * p.Hkv : 0, k)) u += 32;
+            u += k;
+            st.b = u;
+            long long cost = plan[u];
+            if (per == 32) {
+                const int b = u * 32 + lane;
+                const long long c = b < p.B ? seq_cost(p, load_seq(p, b), 0, 1) : 0;
+                find(c * p.Hkv, k);
+                st.b = u * 32 + k;
+                cost = __shfl_sync(0xffffffffu, c, k);
             }
-            const Seq s = lane_seq(g);
-            const long long c = seq_costs(p, s);
-            const long long cum = before + scan_add(c);
-            const int k = __ffs(__ballot_sync(0xffffffffu, cum * p.Hkv > begin)) - 1;
-            Seq o;
-            o.s0 = o.n = 0;
-            o.L = __shfl_sync(0xffffffffu, s.L, k);
-            o.rows = __shfl_sync(0xffffffffu, s.rows, k);
-            o.tiles = __shfl_sync(0xffffffffu, s.tiles, k);
-            o.bad = __shfl_sync(0xffffffffu, s.bad ? 1 : 0, k) != 0;
-            const long long cost = __shfl_sync(0xffffffffu, c, k);
-            before = __shfl_sync(0xffffffffu, cum - c, k) * p.Hkv;
-            st.b = g * 32 + k;
-            st.kvh = static_cast<int>((begin - before) / cost);
+            const Seq s = load_seq(p, st.b);
+            st.kvh = static_cast<int>(static_cast<double>(begin - before) / cost);
+            if ((st.kvh + 1) * cost <= begin - before) ++st.kvh;     // (the division's rounding)
+            if (st.kvh * cost > begin - before) --st.kvh;
             before += cost * st.kvh;
-            for (int t = 0;; t += 32) {
-                const long long ic = t + lane < o.tiles ? item_cost(p, item_of(p, o, t + lane)) : 0;
-                const long long icum = before + scan_add(ic);
-                const uint32_t past = __ballot_sync(0xffffffffu, icum > begin);
-                if (past) {
-                    const int i = __ffs(past) - 1;
-                    st.tile = t + i;
-                    st.at = __shfl_sync(0xffffffffu, icum - ic, i);
-                    break;
-                }
-                before = __shfl_sync(0xffffffffu, icum, 31);
-            }
+            while (!find(st.tile + lane < s.tiles ? item_cost(p, item_of(p, s, st.tile + lane)) : 0, k)) st.tile += 32;
+            st.tile += k;
+            st.at = before;
         }
         if (lane == 0) *out = st;
     }
@@ -406,6 +411,7 @@ __device__ __forceinline__ long long slot_row(const ChunkParams &p, int cta, int
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                 const __grid_constant__ ChunkParams p) {
     using C = Cfg<D, Q8>;
     extern __shared__ uint8_t smem_raw[];
@@ -414,21 +420,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 1, *o_full = bars + 2, *o_empty = bars + 3, *drain = bars + 4;
-    uint64_t *k_full = bars + 5, *k_empty = k_full + C::NK, *v_full = k_empty + C::NK, *v_empty = v_full + C::NV;
-    uint64_t *v_fix = v_empty + C::NV, *s_full = v_fix + C::NV, *p_ready = s_full + 2;
+    uint64_t *k_full = bars + 5, *k_empty = k_full + C::NK, *k_raw = k_empty + C::NK;
+    uint64_t *v_full = k_raw + C::NK, *v_empty = v_full + C::NV, *v_raw = v_empty + C::NV;
+    uint64_t *s_full = v_raw + C::NV, *p_ready = s_full + 2;
     uint32_t *s_poison = reinterpret_cast<uint32_t *>(smem + C::OFF_POISON);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
-    int *s_parent = reinterpret_cast<int *>(smem + C::OFF_PARENT);
+    int16_t *s_parent = reinterpret_cast<int16_t *>(smem + C::OFF_PARENT);
+    uint8_t *s_scale = smem + C::OFF_SCALE;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 8);                       // one arrive per softmax warp
         mbar_init(q_empty, 1);
         mbar_init(o_full, 1);
         mbar_init(o_empty, 8);
-        for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 4 : 1); mbar_init(k_empty + i, 1); }
-        for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 4 : 1); mbar_init(v_empty + i, 1); mbar_init(v_fix + i, 1); }
+        // (one arrive per loader warp, by TMA or by the fixer)
+        for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 8 : 1); mbar_init(k_empty + i, 1); mbar_init(k_raw + i, 1); }
+        for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 8 : 1); mbar_init(v_empty + i, 1); mbar_init(v_raw + i, 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(s_full + i, 1); mbar_init(p_ready + i, 4); }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -472,64 +481,80 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     };
 
     Walk w;
-    const int bs = p.cache.block_size;
+    const int bs = p.cache.block_size, bsh = __ffs(bs) - 1;
 
     if (warp == kWarpK || warp == kWarpV) {
-        // ------------------------------------------ TMA producers (bf16 cache)
+        // ---------------------------------------------------- TMA producers
         regs_dec<C::REGS_OTHER>();
-        if constexpr (!Q8) {
-            const bool is_k = warp == kWarpK;
-            const int ns = is_k ? C::NK : C::NV;
-            uint8_t *ring = smem + (is_k ? C::OFF_K : C::OFF_V);
-            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
-            const CUtensorMap *map = is_k ? &tm_k : &tm_v;
-            if (lane == 0) tma_prefetch_desc(map);
-            const int nb = 128 / bs;
-            int st = 0, ph = 1, issued = 0;
-            bool ok = true;
-            w.start(p, s_start);
-            while (ok && w.next(p)) {
-                const int32_t *row = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
-                const int first = w.it.lo / bs, last = (w.it.hi - 1) / bs;
-                // blocks outside the item's keys are not looked up: their rows
-                // repeat a block inside (masked, and zeroed in V)
-                auto fetch = [&](int j) {
-                    return lane < nb && w.it.hi > 0 ? row[min(max(w.key0(j) / bs + lane, first), last)] : 0;
-                };
-                int id = fetch(w.j0);
-                for (int j = w.j0; j < w.j1; ++j) {
-                    if (!warp_wait(empty + st, ph)) { ok = false; break; }
-                    if (w.it.hi == 0) {             // nothing to read: a wholly masked tile
-                        if (lane == 0) mbar_arrive(full + st);
-                    } else {
-                        if (lane == 0) mbar_arrive_expect_tx(full + st, C::TILE);
-                        __syncwarp();
-                        if (lane < nb) {
-                            int n = id;
-                            if (n < 0 || n >= p.cache.num_blocks) {
-                                raise_status(p.status, kStatusBadBlock);
-                                n = 0;
+        const bool is_k = warp == kWarpK;
+        const int ns = is_k ? C::NK : C::NV;
+        uint8_t *ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+        // K tiles of a bf16 cache go straight to the MMAs, the others by the loaders or the fixer
+        uint64_t *full = is_k ? (Q8 ? k_raw : k_full) : v_raw, *empty = is_k ? k_empty : v_empty;
+        const CUtensorMap *map = is_k ? &tm_k : &tm_v, *tree_map = is_k ? &tm_kt : &tm_vt;
+        if (lane == 0) tma_prefetch_desc(map);
+        const int nb = 128 >> bsh;
+        int st = 0, ph = 1, issued = 0;
+        bool ok = true;
+        w.start(p, s_start);
+        while (ok && w.next(p)) {
+            const int32_t *row = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
+            const int first = w.it.lo >> bsh, last = (w.it.hi - 1) >> bsh;
+            // blocks outside the item's keys are not looked up: their rows
+            // repeat a block inside (masked, and zeroed in V)
+            auto fetch = [&](int j) {
+                return lane < nb && w.it.hi > 0 && j < w.it.cache_tiles
+                           ? row[min(max((w.key0(j) >> bsh) + lane, first), last)] : 0;
+            };
+            int id = fetch(w.j0);
+            for (int j = w.j0; j < w.j1; ++j) {
+                if (!warp_wait(empty + st, ph)) { ok = false; break; }
+                uint8_t *stage = ring + st * C::TILE;
+                if (j >= w.it.cache_tiles) {            // rows of the tree (behind them: other trees', or zeros)
+                    if (Q8 && lane == 0) {
+                        mbar_arrive_expect_tx(full + st, C::TILE);
+                        const int y = (w.cur_b * p.Hkv + w.cur_kvh) * p.N + (j - w.it.cache_tiles) * 128;
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h) tma_load_2d(stage + h * C::BOX, tree_map, full + st, h * 64, y);
+                    }
+                } else if (w.it.hi == 0) {              // nothing to read: a wholly masked tile
+                    if (lane == 0) mbar_arrive(full + st);
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(full + st, Q8 ? C::RAW + (is_k ? 256 : 0) : C::TILE);
+                    __syncwarp();
+                    if (lane < nb) {
+                        int n = id;
+                        if (n < 0 || n >= p.cache.num_blocks) {
+                            raise_status(p.status, kStatusBadBlock);
+                            n = 0;
+                        }
+                        const int y = (n * p.Hkv + w.cur_kvh) << bsh;
+                        if constexpr (Q8) {
+                            tma_load_2d(stage + C::TILE - C::RAW + (lane << bsh) * D, map, full + st, 0, y);
+                            if (is_k) {                 // the scale bytes of both come with K
+                                uint8_t *sc = s_scale + st * 256 + (lane << bsh);
+                                bulk_load(sc, p.cache.k_scale + y, bs, full + st);
+                                bulk_load(sc + 128, p.cache.v_scale + y, bs, full + st);
                             }
-                            const int y = (n * p.Hkv + w.cur_kvh) * bs;
-                            uint8_t *stage = ring + st * C::TILE + lane * bs * 128;
+                        } else {
 #pragma unroll
                             for (int h = 0; h < C::HALVES; ++h)
-                                tma_load_2d(stage + h * C::BOX, map, full + st, h * 64, y);
+                                tma_load_2d(stage + h * C::BOX + (lane << bsh) * 128, map, full + st, h * 64, y);
                         }
                     }
-                    if (j + 1 < w.j1) id = fetch(j + 1);
-                    ++issued;
-                    if (++st == ns) { st = 0; ph ^= 1; }
                 }
+                id = fetch(j + 1);
+                ++issued;
+                if (++st == ns) { st = 0; ph ^= 1; }
             }
-            __syncwarp();
-            if (lane == 0 && *s_abort)              // let the copies in flight land
-                for (int i = max(0, issued - ns); i < issued; ++i) mbar_wait(full + i % ns, (i / ns) & 1);
         }
+        __syncwarp();
+        if (lane == 0 && *s_abort)                      // let the copies in flight land
+            for (int i = max(0, issued - ns); i < issued; ++i) mbar_wait(full + i % ns, (i / ns) & 1);
         __syncwarp();
     } else if (warp == kWarpFix) {
         // ------------------- partly visible V tiles of a bf16 cache, in place
-        // (every tile passes here, so that the phases of v_fix follow the ring)
+        // (every tile passes here, so that the phases of v_full follow the ring)
         regs_dec<C::REGS_OTHER>();
         if constexpr (!Q8) {
             int pos = 0;
@@ -538,9 +563,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             while (ok && w.next(p)) {
                 for (int j = w.j0; j < w.j1; ++j, ++pos) {
                     const int st = pos % C::NV;
-                    if (!warp_wait(v_full + st, pos / C::NV)) { ok = false; break; }
+                    if (!warp_wait(v_raw + st, pos / C::NV)) { ok = false; break; }
                     if (!w.partial(j)) {
-                        if (lane == 0) mbar_arrive(v_fix + st);
+                        if (lane == 0) mbar_arrive(v_full + st);
                         continue;
                     }
                     uint8_t *sv = smem + C::OFF_V + st * C::TILE;
@@ -576,7 +601,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(v_fix + st);
+                    if (lane == 0) mbar_arrive(v_full + st);
                 }
             }
         }
@@ -625,7 +650,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             for (int s = 0; ok && s < n_steps; ++s) {
                 const int g = s & 1;
                 if (!two || g == 0) {
-                    ok = warp_wait((Q8 ? v_full : v_fix) + vst, vph);
+                    ok = warp_wait(v_full + vst, vph);
                 }
                 if (ok) ok = warp_wait(p_ready + g, g ? cnt1 : cnt0);
                 if (!ok) break;
@@ -649,159 +674,119 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (elect_one()) mma_commit(drain);         // all MMAs issued are done before TMEM is freed
         warp_wait(drain, 0);
     } else if (warp >= kWarpLoad) {
-        // --------------------------------------------- loaders (e4m3 cache)
+        // -------------------------------------------- loaders (e4m3 cache)
         if constexpr (Q8) {
             regs_dec<C::REGS_LOAD>();
-            constexpr int LPR = D / 16;             // lanes per cache row (16 codes each)
-            constexpr int RPR = 128 / LPR;          // rows a round of the four warps covers: 16 (D = 128) or 32
-            constexpr int ROUNDS = 128 / RPR;
-            const int lw = warp - kWarpLoad;
-            const int row_in = lw * (32 / LPR) + lane / LPR, c = lane % LPR;
-            int kst = 0, kph = 1, vst = 0, vph = 1, pos = 0;
+            constexpr int LPR = D / 8;              // lanes per cache row (8 codes each)
+            constexpr int RW = 32 / LPR;            // rows of a warp and round
+            constexpr int ROUNDS = 16 / RW;         // a warp has 16 rows of a tile
+            const int lw = warp - kWarpLoad, c = lane % LPR;
+            // row of (round, row in the round); rows of one round are 8 * RW apart from the next's,
+            // so a lane's place in the swizzle is the same in every round
+            auto row_of = [&](int i, int k) { return i * 8 * RW + lw * RW + k; };
+            const int row0 = row_of(0, lane / LPR);
+            const uint32_t raw_off = C::TILE - C::RAW + row0 * D + c * 8;
+            const uint32_t out_off = (c >> 3) * C::BOX + row0 * 128 + (((c & 7) ^ (row0 & 7)) << 4);
+            Walk &lwk = *reinterpret_cast<Walk *>(smem + C::OFF_WALK + C::WALK_BYTES);
+            volatile int *more = reinterpret_cast<volatile int *>(smem + C::OFF_WALK + 2 * C::WALK_BYTES - 4);
+            const bool first_thread = threadIdx.x == kWarpLoad * 32;
+            int kst = 0, kph = 0, vst = 0, vph = 0, pos = 0;
             bool ok = true;
-            struct Regs { uint4 u[ROUNDS]; uint32_t e[(ROUNDS + 3) / 4]; };
-            const int nb = 128 / bs;
-            w.start(p, s_start);
-            while (ok && w.next(p)) {
-                const int32_t *trow = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
-                auto cached = [&](int j) { return j < w.it.cache_tiles; };
-                // blocks of a tile, lane i holding the i-th (outside the item's
-                // keys: one inside, whose rows are not read)
-                const int first_b = w.it.lo / bs, last_b = max(w.it.hi - 1, 0) / bs;
-                auto fetch = [&](int j) {
-                    if (lane >= nb || w.it.hi == 0 || !cached(j)) return 0;
-                    return static_cast<int>(trow[min(max(w.key0(j) / bs + lane, first_b), last_b)]);
-                };
-                auto checked = [&](int n) {
-                    if (n < 0 || n >= p.cache.num_blocks) {
-                        raise_status(p.status, kStatusBadBlock);
-                        n = 0;
-                    }
-                    return n;
-                };
-                // codes and scale bytes of one tile into registers; rows outside
-                // [lo, hi) are not read
-                auto load = [&](int j, int ids, bool is_v, Regs &r) {
-                    const uint8_t *src = static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k);
-                    const uint8_t *sc = is_v ? p.cache.v_scale : p.cache.k_scale;
+            if (first_thread) lwk.start(p, s_start);
+            // a stage's codes to bf16, in place; lane l < 16 holds the multiplier
+            // of row (l / RW, l % RW), 0 for rows that are no keys
+            auto convert = [&](uint8_t *stage, uint32_t mult) {
+                uint2 u[ROUNDS];
 #pragma unroll
-                    for (int i = 0; i < (ROUNDS + 3) / 4; ++i) r.e[i] = 0;
+                for (int i = 0; i < ROUNDS; ++i) u[i] = *reinterpret_cast<const uint2 *>(stage + raw_off + i * 8 * RW * D);
+                bar_sync(2, 256);                   // all codes are in registers
 #pragma unroll
-                    for (int i = 0; i < ROUNDS; ++i) {
-                        const int at = i * RPR + row_in, key = w.key0(j) + at;
-                        const int n = __shfl_sync(0xffffffffu, ids, at / bs);
-                        r.u[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (key >= w.it.lo && key < w.it.hi) {
-                            const size_t row = (static_cast<size_t>(n) * p.Hkv + w.cur_kvh) * bs + at % bs;
-                            r.u[i] = *reinterpret_cast<const uint4 *>(src + row * D + c * 16);
-                            r.e[i / 4] |= static_cast<uint32_t>(sc[row]) << (8 * (i % 4));
-                        }
-                    }
-                };
-                // bf16 rows of a swizzled tile from codes
-                auto store = [&](uint8_t *tile, const Regs &r, bool is_v) {
-#pragma unroll
-                    for (int i = 0; i < ROUNDS; ++i) {
-                        const int key = i * RPR + row_in;
-                        int e = (r.e[i / 4] >> (8 * (i % 4))) & 255;
-                        uint4 u = r.u[i];
-                        if (is_v && e == kScaleNan) { u = make_uint4(0u, 0u, 0u, 0u); e = kScaleMin; }
-                        const uint32_t mult = e4m3_mult(e);
-                        const uint2 a = dequant_e4m3x4(u.x, mult), b = dequant_e4m3x4(u.y, mult);
-                        const uint2 d = dequant_e4m3x4(u.z, mult), f = dequant_e4m3x4(u.w, mult);
-                        uint4 x = make_uint4(a.x, a.y, b.x, b.y), y = make_uint4(d.x, d.y, f.x, f.y);
-                        // 16-byte pieces 2c and 2c+1 of the row; lanes of the two 64-column
-                        // halves write them in opposite order, so that eight lanes of a row
-                        // meet eight different bank groups
-                        const int q0 = 2 * c, half = q0 >> 3;
-                        int first = q0 & 7, second = first + 1;
-                        if (half) {
-                            const uint4 t = x; x = y; y = t;
-                            const int o = first; first = second; second = o;
-                        }
-                        uint8_t *rp = tile + half * C::BOX + key * 128;
-                        *reinterpret_cast<uint4 *>(rp + ((first ^ (key & 7)) << 4)) = x;
-                        *reinterpret_cast<uint4 *>(rp + ((second ^ (key & 7)) << 4)) = y;
-                    }
-                };
-                // scale byte of V row lw * 32 + lane of cache tile j: rows held as NaN
-                // are told to the softmax groups with the tile's K
-                auto v_byte = [&](int j, int ids) {
-                    const int at = lw * 32 + lane, key = w.key0(j) + at;
-                    const int n = __shfl_sync(0xffffffffu, ids, at / bs);
-                    return key >= w.it.lo && key < w.it.hi
-                               ? static_cast<int>(p.cache.v_scale[(static_cast<size_t>(n) * p.Hkv + w.cur_kvh) * bs + at % bs])
-                               : 0;
-                };
-                // tree rows (bf16, contiguous): 16 lanes a row at D = 128, 8 at D = 64
-                auto tree_tile = [&](int j, const __nv_bfloat16 *src, uint8_t *tile, bool is_v, int at) {
-                    constexpr int L2 = D / 8, R2 = 32 / L2;      // lanes per row, rows per warp and round
-                    const int cc = lane % L2, key_first = (j - w.it.cache_tiles) * 128;
-                    uint32_t word = 0;
-                    for (int i = 0; i < 32 / R2; ++i) {
-                        const int rr = lw * 32 + i * R2 + lane / L2;   // row of the tile; a warp has 32 of them
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (key_first + rr < p.N)
-                            u = *reinterpret_cast<const uint4 *>(
-                                src + ((static_cast<size_t>(w.cur_b) * p.Hkv + w.cur_kvh) * p.N + key_first + rr) * D + cc * 8);
-                        if (is_v) {
-                            uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                                  __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
-                            const uint32_t lanes = __ballot_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
-                            const uint32_t mine = (lanes >> (lane / L2 * L2)) & ((1ull << L2) - 1);
-                            if (mine) u = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                            for (int g = 0; g < R2; ++g)
-                                if ((lanes >> (g * L2)) & ((1ull << L2) - 1)) word |= 1u << (i * R2 + g);
-                        }
-                        if (tile)
-                            *reinterpret_cast<uint4 *>(tile + (cc >> 3) * C::BOX + rr * 128 + (((cc & 7) ^ (rr & 7)) << 4)) = u;
-                    }
-                    if (at >= 0 && lane == 0) s_poison[at * 4 + lw] = word;
-                };
-                auto publish = [&](uint64_t *full) {
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full);
-                };
-                // fill order K0 K1 V0 K2 V1 ...: the unit after next is on its way
-                // from memory while this one is converted
-                Regs rk, rv;
-                int id_k = checked(fetch(w.j0)), id_v = id_k, id_next = fetch(w.j0 + 1), vb = 0;
-                if (cached(w.j0)) {
-                    load(w.j0, id_k, false, rk);
-                    vb = v_byte(w.j0, id_k);
+                for (int i = 0; i < ROUNDS; ++i) {
+                    const uint32_t m = __shfl_sync(0xffffffffu, mult, i * RW + lane / LPR);
+                    const uint2 a = dequant_e4m3x4(u[i].x, m), b = dequant_e4m3x4(u[i].y, m);
+                    *reinterpret_cast<uint4 *>(stage + out_off + i * 8 * RW * 128) = make_uint4(a.x, a.y, b.x, b.y);
                 }
-                for (int j = w.j0; j <= w.j1; ++j) {
-                    if (j > w.j0 && cached(j - 1)) load(j - 1, id_v, true, rv);
-                    if (j < w.j1) {
-                        if (!warp_wait(k_empty + kst, kph)) { ok = false; break; }
-                        uint8_t *tile = smem + C::OFF_K + kst * C::TILE;
-                        const int at = pos % kPoisonRing;
-                        if (cached(j)) {
-                            const uint32_t word = __ballot_sync(0xffffffffu, vb == kScaleNan);
-                            if (lane == 0) s_poison[at * 4 + lw] = word;
-                            store(tile, rk, false);
+            };
+            auto publish = [&](uint64_t *full) {
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            };
+            for (;;) {
+                bar_sync(2, 256);
+                if (first_thread) *more = lwk.next(p);
+                bar_sync(2, 256);
+                if (!*more) break;
+                const int j0 = lwk.j0, j1 = lwk.j1, cache_tiles = lwk.it.cache_tiles;
+                const int lo = lwk.it.lo, hi = lwk.it.hi, base = lwk.it.base;
+                uint32_t v_mult = 0;
+                // fill order K0 K1 V0 K2 V1 ...
+                for (int j = j0; j <= j1; ++j) {
+                    if (j < j1) {
+                        const int at = (pos % kPoisonRing) * 4;
+                        uint8_t *stage = smem + C::OFF_K + kst * C::TILE;
+                        if (ok) ok = warp_wait(k_raw + kst, kph);
+                        if (j < cache_tiles) {
+                            const uint8_t *sc = s_scale + kst * 256;
+                            const int a = lo - (base + j * 128), z = hi - (base + j * 128);     // live rows [a, z)
+                            const int r = row_of((lane & 15) / RW, (lane & 15) % RW);
+                            const bool live = r >= a && r < z;
+                            const uint32_t k_mult = live ? e4m3_mult(sc[r]) : 0u;
+                            // V rows held as NaN are zeroed and told to the softmax groups
+                            const int ev = sc[128 + r];
+                            const uint32_t v_next = live && ev != kScaleNan ? e4m3_mult(ev) : 0u;
+                            const int r4 = (lw & 3) * 32 + lane;
+                            const uint32_t word = __ballot_sync(0xffffffffu, r4 >= a && r4 < z && sc[128 + r4] == kScaleNan);
+                            if (lw < 4 && lane == 0) s_poison[at + lw] = word;
+                            convert(stage, k_mult);
+                            publish(k_full + kst);
+                            if (j > j0) {           // (V of the tile before still needs its own)
+                                const uint32_t t = v_mult;
+                                v_mult = v_next;
+                                uint8_t *vs = smem + C::OFF_V + vst * C::TILE;
+                                if (ok) ok = warp_wait(v_raw + vst, vph);
+                                convert(vs, t);
+                                publish(v_full + vst);
+                                if (++vst == C::NV) { vst = 0; vph ^= 1; }
+                            } else {
+                                v_mult = v_next;
+                            }
                         } else {
-                            tree_tile(j, p.k_tree, tile, false, -1);
-                            tree_tile(j, p.v_tree, nullptr, true, at);
+                            publish(k_full + kst);  // (rows behind the tree are masked)
                         }
-                        publish(k_full + kst);
                         if (++kst == C::NK) { kst = 0; kph ^= 1; }
                         ++pos;
-                        id_v = id_k;
-                        if (j + 1 < w.j1 && cached(j + 1)) {
-                            id_k = checked(id_next);
-                            id_next = fetch(j + 2);
-                            load(j + 1, id_k, false, rk);
-                            vb = v_byte(j + 1, id_k);
-                        }
+                        if (j < cache_tiles) continue;
                     }
-                    if (j > w.j0) {
-                        if (!warp_wait(v_empty + vst, vph)) { ok = false; break; }
-                        uint8_t *tile = smem + C::OFF_V + vst * C::TILE;
-                        if (cached(j - 1)) store(tile, rv, true);
-                        else tree_tile(j - 1, p.v_tree, tile, true, -1);
+                    if (j > j0) {                   // V of tile j - 1 where tile j is not a cache tile
+                        uint8_t *vs = smem + C::OFF_V + vst * C::TILE;
+                        if (ok) ok = warp_wait(v_raw + vst, vph);
+                        if (j - 1 < cache_tiles) {
+                            convert(vs, v_mult);
+                        } else {
+                            // tree rows: 16 a warp, two lanes a row; rows behind the tree are
+                            // zeroed, and so are rows with an infinity or a NaN, which are told
+                            // to the softmax groups (they wait for this tile)
+                            const int at = ((pos - (j < j1 ? 2 : 1)) % kPoisonRing) * 4;
+                            const int r = lw * 16 + (lane >> 1), live = min(128, p.N - (j - 1 - cache_tiles) * 128);
+                            uint8_t *rp = vs + r * 128;
+                            uint32_t big = 0;
+                            for (int x = lane & 1; x < D / 8; x += 2) {
+                                const uint4 u = *reinterpret_cast<const uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4));
+                                big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
+                                big = __vmaxu2(big, u.w & 0x7fff7fffu);
+                            }
+                            big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                            const bool inf = r < live && max(big & 0xffffu, big >> 16) >= 0x7f80u;
+                            if (r >= live || inf)
+                                for (int x = lane & 1; x < D / 8; x += 2)
+                                    *reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            uint32_t half = 0;      // a bit per row of the warp
+                            const uint32_t bits = __ballot_sync(0xffffffffu, inf);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) half |= ((bits >> (2 * x)) & 1u) << x;
+                            if (lane == 0) reinterpret_cast<uint16_t *>(s_poison + at)[lw] = static_cast<uint16_t>(half);
+                        }
                         publish(v_full + vst);
                         if (++vst == C::NV) { vst = 0; vph ^= 1; }
                     }
@@ -820,10 +805,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const float c2 = p.scale_log2, nan = __int_as_float(0x7fc00000);
         int cnt = 0, items = 0, pos = 0;                    // steps of this group, items, key tiles so far
         bool ok = true;
-        w.start(p, s_start);
+        // One walk for both groups, in shared memory: its thirty values would
+        // cost every softmax thread as many registers.
+        static_assert(sizeof(Walk) + 4 <= C::WALK_BYTES, "shared memory of the walk");
+        Walk &w = *reinterpret_cast<Walk *>(smem + C::OFF_WALK);
+        volatile int *more = reinterpret_cast<volatile int *>(smem + C::OFF_WALK + C::WALK_BYTES - 4);
+        const bool first_thread = threadIdx.x == kWarpSoftmax * 32;
+        if (first_thread) w.start(p, s_start);
         // both partial slots' headers are written by every launch
         int head_first = -1, head_last = -1;
-        while (w.next(p)) {
+        for (;;) {
+            if (first_thread) *more = w.next(p);
+            bar_sync(1, 256);
+            if (!*more) break;
             const int two = w.it.two;
             const int row = two ? grp * 128 + r : r;        // row of the item
             const bool valid = row < w.it.rows;
@@ -837,13 +831,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 orow = (static_cast<size_t>(w.cur_b) * p.Hq + static_cast<size_t>(w.cur_kvh) * p.G) * p.N + pr;
                 qp = p.q + orow * D;
             } else {
-                t = pr / p.G;
+                t = div_g(p, pr);
                 g = pr - t * p.G;
                 const int h = w.cur_kvh * p.G + g;
                 orow = static_cast<size_t>(w.s.s0 + t) * p.Hq + h;
                 qp = p.q + (w.s.s0 + t) * p.q_stride + static_cast<size_t>(h) * D;
             }
-            if (w.s.bad && threadIdx.x == kWarpSoftmax * 32) raise_status(p.status, kStatusPrefixLenRange);
+            if (w.s.bad && first_thread) raise_status(p.status, kStatusPrefixLenRange);
             bool row_nan = w.s.bad;
             // ---- Q into shared memory (one row tile: each group half of the columns)
             {
@@ -867,12 +861,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             bool tree_bad = false;
             if (w.j1 > w.it.cache_tiles) {                  // this CTA has keys of the tree
                 const int i = (warp - kWarpSoftmax) * 32 + lane;
-                bar_sync(1, 256);                           // the last item's walks are over
                 bool bad = false;
                 if (i < p.N) {
                     const int up = p.parent[static_cast<size_t>(w.cur_b) * p.N + i];
                     bad = up < -1 || up >= i;
-                    s_parent[i] = up;
+                    s_parent[i] = static_cast<int16_t>(up);
                 }
                 __syncwarp();
                 tree_bad = bar_or(1, 256, bad);
@@ -892,22 +885,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 ++cnt;
                 tc_fence_after();
                 if (ok && warp_active) {
-                    uint32_t r0[32], r1[32], r2[32], r3[32];
-                    tmem_ld32(t_s + 0, r0);
-                    tmem_ld32(t_s + 32, r1);
-                    tmem_ld32(t_s + 64, r2);
-                    tmem_ld32(t_s + 96, r3);
+                    // the keys of a partly visible tile that this row sees
                     const bool of_tree = j >= w.it.cache_tiles;
+                    const bool masked = of_tree || w.partial(j);
+                    uint32_t see[4];
                     uint4 bad_v = make_uint4(0u, 0u, 0u, 0u);
-                    if (Q8) bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
-                    tmem_wait_ld();
-                    if (of_tree || w.partial(j)) {
-                        uint32_t see[4];
+                    if (Q8 && !of_tree) bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
+                    if (masked) {
                         if (of_tree) {
                             const int first = (j - w.it.cache_tiles) * 128;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see[i] = 0;
-                            for (int node = tree_bad ? -1 : t; node >= 0; node = s_parent[node]) {   // (parents lie below their nodes)
+                            // (parents lie below their nodes, so the walk ends)
+                            for (int node = tree_bad ? -1 : t; node >= 0; node = s_parent[node]) {
                                 const int d = node - first;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) see[i] |= (d >> 5) == i ? 1u << (d & 31) : 0u;
@@ -916,34 +906,62 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             const int a = row_lo - w.key0(j), z = row_hi - w.key0(j);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see[i] = bit_range(a - 32 * i, z - 32 * i);
-                            if (!Q8) {
-                                // the fixer's word on this tile
-                                ok = warp_wait(v_fix + (pos + jj) % C::NV, (pos + jj) / C::NV);
-                                bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
-                            }
                         }
-                        const uint32_t ninf = __float_as_uint(-INFINITY);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            r0[i] = (see[0] >> i) & 1u ? r0[i] : ninf;
-                            r1[i] = (see[1] >> i) & 1u ? r1[i] : ninf;
-                            r2[i] = (see[2] >> i) & 1u ? r2[i] : ninf;
-                            r3[i] = (see[3] >> i) & 1u ? r3[i] : ninf;
+                        if (!Q8 || of_tree) {           // the fixer's or the loaders' word on this tile
+                            __syncwarp();
+                            ok = warp_wait(v_full + (pos + jj) % C::NV, (pos + jj) / C::NV);
+                            bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
                         }
-                        __syncwarp();
                         if ((see[0] & bad_v.x) | (see[1] & bad_v.y) | (see[2] & bad_v.z) | (see[3] & bad_v.w)) row_nan = true;
+                        __syncwarp();
                     } else if (Q8) {
                         if (bad_v.x | bad_v.y | bad_v.z | bad_v.w) row_nan = true;
                     }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto hide = [&](uint32_t (&sc)[32], int q) {
+                        if (masked) {
+                            const uint32_t ninf = __float_as_uint(-INFINITY);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        m4[0] = max3(m4[0], __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
-                        m4[1] = max3(m4[1], __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
-                        m4[2] = max3(m4[2], __uint_as_float(r2[i]), __uint_as_float(r2[i + 1]));
-                        m4[3] = max3(m4[3], __uint_as_float(r3[i]), __uint_as_float(r3[i + 1]));
+                            for (int i = 0; i < 32; ++i) sc[i] = (see[q] >> i) & 1u ? sc[i] : ninf;
+                        }
+                    };
+                    auto max32 = [&](const uint32_t (&sc)[32]) {
+                        float a = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            a = max3(a, __uint_as_float(sc[i]), __uint_as_float(sc[i + 1]));
+                            b2 = max3(b2, __uint_as_float(sc[i + 2]), __uint_as_float(sc[i + 3]));
+                        }
+                        return max3(a, b2, -INFINITY);
+                    };
+                    // bf16 caches: the row's 128 scores stay in registers; e4m3: they
+                    // are read twice, which leaves the loaders their registers
+                    uint32_t r0[32], r1[32], r2[32], r3[32];
+                    float m_tile;
+                    if constexpr (!Q8) {
+                        tmem_ld32(t_s + 0, r0);
+                        tmem_ld32(t_s + 32, r1);
+                        tmem_ld32(t_s + 64, r2);
+                        tmem_ld32(t_s + 96, r3);
+                        tmem_wait_ld();
+                        hide(r0, 0);
+                        hide(r1, 1);
+                        hide(r2, 2);
+                        hide(r3, 3);
+                        m_tile = max3(max3(max32(r0), max32(r1), max32(r2)), max32(r3), -INFINITY) * c2;
+                    } else {
+                        tmem_ld32(t_s + 0, r0);
+                        tmem_ld32(t_s + 32, r1);
+                        tmem_wait_ld();
+                        hide(r0, 0);
+                        hide(r1, 1);
+                        m_tile = max3(max32(r0), max32(r1), -INFINITY);
+                        tmem_ld32(t_s + 64, r0);
+                        tmem_ld32(t_s + 96, r1);
+                        tmem_wait_ld();
+                        hide(r0, 2);
+                        hide(r1, 3);
+                        m_tile = max3(m_tile, max32(r0), max32(r1)) * c2;
                     }
-                    const float m_tile = max3(max3(m4[0], m4[1], m4[2]), m4[3], -INFINITY) * c2;
                     if (m_tile != m_tile) row_nan = true;
                     const float m_new = fmaxf(m_run, m_tile);
                     bool resc = false;
@@ -974,10 +992,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         }
                         tmem_st16(t_s + col, pk);
                     };
-                    exps(r0, 0);
-                    exps(r1, 16);
-                    exps(r2, 32);
-                    exps(r3, 48);
+                    if constexpr (!Q8) {
+                        exps(r0, 0);
+                        exps(r1, 16);
+                        exps(r2, 32);
+                        exps(r3, 48);
+                    } else {
+                        // P lands on columns 0..63, whose scores are in registers by then
+                        tmem_ld32(t_s + 0, r0);
+                        tmem_ld32(t_s + 32, r1);
+                        tmem_wait_ld();
+                        hide(r0, 0);
+                        hide(r1, 1);
+                        exps(r0, 0);
+                        exps(r1, 16);
+                        tmem_ld32(t_s + 64, r0);
+                        tmem_ld32(t_s + 96, r1);
+                        tmem_wait_ld();
+                        hide(r0, 2);
+                        hide(r1, 3);
+                        exps(r0, 32);
+                        exps(r1, 48);
+                    }
                     if (__any_sync(0xffffffffu, resc)) {
                         // this tile's scores were committed after P*V of the group's previous
                         // tile, so O[grp] is complete, and P*V of this tile waits for this warp
@@ -1022,7 +1058,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 l = a0 * l0 + a1 * l1;
                 row_nan = l0 != l0 || l1 != l1;
                 has1 = n_tiles > 1;
-                bar_sync(1, 256);                           // read before the next item's Q lands there
             } else if (!ok) {
                 row_nan = true;
             }
@@ -1070,22 +1105,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
-            if (!whole && threadIdx.x == kWarpSoftmax * 32) {
+            if (!whole && first_thread) {
                 PartHead hd;
                 hd.b = w.cur_b;
                 hd.kvh = w.cur_kvh;
                 hd.r0 = w.it.r0;
                 hd.rows = w.it.rows;
                 hd.s0 = w.s.s0;
-                hd.last = w.j1 == w.it.nt;
+                // segments: the CTA that holds the item's last tile is the last one
+                const long long tail = w.at - (two ? p.c2 : p.c1), share = s_start->end - s_start->begin;
+                int more_ctas = 0;
+                for (long long e = w.end; e <= tail; e += share) ++more_ctas;
+                hd.n = 1 + more_ctas;
                 hd.pad0 = hd.pad1 = 0;
                 p.heads[2 * blockIdx.x + which] = hd;
                 if (which == 0) head_first = 1; else head_last = 1;
             }
             ++items;
             pos += n_tiles;
+            bar_sync(1, 256);       // the item's fields, parents and exchanged sums are read; the next may come
         }
-        if (threadIdx.x == kWarpSoftmax * 32) {
+        if (first_thread) {
             if (head_first < 0) p.heads[2 * blockIdx.x].rows = 0;
             if (head_last < 0) p.heads[2 * blockIdx.x + 1].rows = 0;
         }
@@ -1101,8 +1141,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
 // -------------------------------------------------------------------- merge
 // Rows of items that crossed CTA borders: the partials of an item are slot 1
-// of the CTA it begins in and slots 0 of the next ones.  One warp per row:
+// of the CTA it begins in and slots 0 of the next n - 1.  One warp per row:
 //   out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M},  lse = M + ln(sum).
+// Bound by latency: the header, then all lse and the first eight partial
+// rows in one round of loads.
 template <int D>
 __global__ void __launch_bounds__(256)
 chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
@@ -1111,78 +1153,82 @@ chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
     const PartHead hd = p.heads[2 * cta + 1];
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (row >= hd.rows) return;
-    int n = 1;                                  // partials: CTAs cta .. cta + n - 1
-    if (!hd.last)
-        for (int c = cta + 1;; c += 32) {       // the first CTA whose segment is the item's last
-            const bool last = c + lane < p.grid ? p.heads[2 * (c + lane)].last != 0 || p.heads[2 * (c + lane)].rows == 0 : true;
-            const uint32_t m = __ballot_sync(0xffffffffu, last);
-            if (m) { n = c + __ffs(m) - 1 - cta + 1; break; }
-        }
-    n = min(n, p.grid - cta);
-    auto slot = [&](int i) { return slot_row(p, cta + i, i == 0 ? 1 : 0) + row; };
-    float mx = -INFINITY;
-    bool bad = false;
-    for (int i = lane; i < n; i += 32) {
-        const float v = p.lse_part[slot(i)];
-        bad |= v != v;
-        mx = fmaxf(mx, v);
-    }
+    const int n = min(hd.n, p.grid - cta);
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < hd.rows; row += gridDim.y * 8) {
+        auto slot = [&](int i) { return slot_row(p, cta + i, i == 0 ? 1 : 0) + row; };
+        float ld[8][DPL];
+        auto load8 = [&](int i0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    bad = __any_sync(0xffffffffu, bad);
-    float acc[DPL], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float wgt = i0 + lane < n ? ex2((p.lse_part[slot(i0 + lane)] - mx) * kLog2e) : 0.f;
-        if (mx == -INFINITY) wgt = 0.f;
-        const int here = min(32, n - i0);
-#pragma unroll 8
-        for (int i = 0; i < here; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wgt, i);
-            const float *src = p.o_part + slot(i0 + i) * D + lane * DPL;
-            float v[DPL];
-            if constexpr (DPL == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(src);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(src);
-                v[0] = x.x; v[1] = x.y;
+            for (int u = 0; u < 8; ++u) {
+                const float *src = p.o_part + slot(min(i0 + u, n - 1)) * D + lane * DPL;
+                if constexpr (DPL == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    ld[u][0] = x.x; ld[u][1] = x.y; ld[u][2] = x.z; ld[u][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    ld[u][0] = x.x; ld[u][1] = x.y;
+                }
             }
-            sum += wi;
-#pragma unroll
-            for (int k = 0; k < DPL; ++k) acc[k] = wi > 0.f ? fmaf(wi, v[k], acc[k]) : acc[k];
+        };
+        load8(0);
+        float mx = -INFINITY, mine = -INFINITY;
+        bool bad = false;
+        for (int i = lane; i < n; i += 32) {
+            const float v = p.lse_part[slot(i)];
+            if (i < 32) mine = v;
+            bad |= v != v;
+            mx = fmaxf(mx, v);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        bad = __any_sync(0xffffffffu, bad);
+        float acc[DPL], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            if (i0 > 0) {
+                load8(i0);
+                if (i0 % 32 == 0) mine = i0 + lane < n ? p.lse_part[slot(i0 + lane)] : -INFINITY;
+            }
+            const float wgt = mx == -INFINITY ? 0.f : ex2((mine - mx) * kLog2e);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float wi = __shfl_sync(0xffffffffu, wgt, (i0 + u) & 31);
+                if (i0 + u < n && wi > 0.f) {   // (a segment without visible keys weighs nothing)
+                    sum += wi;
+#pragma unroll
+                    for (int k = 0; k < DPL; ++k) acc[k] = fmaf(wi, ld[u][k], acc[k]);
+                }
+            }
+        }
+        const float nan = __int_as_float(0x7fc00000);
+        const float inv = bad ? nan : sum > 0.f ? 1.f / sum : 0.f;
+        const float lse = bad ? nan : sum > 0.f ? mx + lg2(sum) * kLn2 : -INFINITY;
+        const int pr = hd.r0 + row;
+        size_t orow;
+        if (p.tree) {
+            orow = (static_cast<size_t>(hd.b) * p.Hq + static_cast<size_t>(hd.kvh) * p.G) * p.N + pr;
+        } else {
+            const int t = div_g(p, pr);
+            orow = static_cast<size_t>(hd.s0 + t) * p.Hq + hd.kvh * p.G + (pr - t * p.G);
+        }
+        __nv_bfloat16 *dst = p.out + orow * D + lane * DPL;
+        if constexpr (DPL == 4) {
+            uint2 pk;
+            pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+            pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+            *reinterpret_cast<uint2 *>(dst) = pk;
+        } else {
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        }
+        if (lane == 0) p.lse[orow] = lse;
     }
-    const float nan = __int_as_float(0x7fc00000);
-    const float inv = bad ? nan : sum > 0.f ? 1.f / sum : 0.f;
-    const float lse = bad ? nan : sum > 0.f ? mx + lg2(sum) * kLn2 : -INFINITY;
-    size_t orow;
-    const int pr = hd.r0 + row;
-    if (p.tree) {
-        orow = (static_cast<size_t>(hd.b) * p.Hq + static_cast<size_t>(hd.kvh) * p.G) * p.N + pr;
-    } else {
-        const int t = pr / p.G;
-        orow = static_cast<size_t>(hd.s0 + t) * p.Hq + hd.kvh * p.G + (pr - t * p.G);
-    }
-    __nv_bfloat16 *dst = p.out + orow * D + lane * DPL;
-    if constexpr (DPL == 4) {
-        uint2 pk;
-        pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<uint2 *>(dst) = pk;
-    } else {
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    }
-    if (lane == 0) p.lse[orow] = lse;
 }
 
 namespace {
 
 template <int D, bool Q8>
-cudaError_t launch(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t stream) {
+cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     using C = Cfg<D, Q8>;
     constexpr int kMaxDev = 64;
     static bool attr_set[kMaxDev] = {};
@@ -1204,9 +1250,10 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensor
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8>, tm_k, tm_v, p);
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8>, tm[0], tm[1], tm[2], tm[3], p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(p.grid, (p.slot_rows + 7) / 8);
+    // (eight blocks of eight rows per CTA make one wave)
+    cfg.gridDim = dim3(p.grid, min(8, (p.slot_rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p);
@@ -1214,16 +1261,18 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap &tm_k, const CUtensor
 
 }  // namespace
 
-cudaError_t launch_chunk_tc(const ChunkParams &p0, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                            cudaStream_t stream) {
+cudaError_t launch_chunk_tc(const ChunkParams &p0, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     ChunkParams p = p0;
     p.c0 = 4;
     p.c1 = 4;
     p.c2 = 8;
     p.min_share = 8;
+    p.g_shift = 0;
+    while ((1 << p.g_shift) < p.G) ++p.g_shift;
+    p.g_mul = static_cast<uint32_t>((1ull << (31 + p.g_shift)) / p.G + 1);
     const bool q8 = p.cache.k_scale != nullptr;
-    if (p.D == 128) return q8 ? launch<128, true>(p, tm_k, tm_v, stream) : launch<128, false>(p, tm_k, tm_v, stream);
-    return q8 ? launch<64, true>(p, tm_k, tm_v, stream) : launch<64, false>(p, tm_k, tm_v, stream);
+    if (p.D == 128) return q8 ? launch<128, true>(p, tm, stream) : launch<128, false>(p, tm, stream);
+    return q8 ? launch<64, true>(p, tm, stream) : launch<64, false>(p, tm, stream);
 }
 
 }  // namespace hta
