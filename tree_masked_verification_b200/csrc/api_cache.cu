@@ -105,7 +105,8 @@ SlotLayout slot_layout(long long packed_rows, int D, int grid) {
 
 // Rows [rows][D] of bf16 in boxes of 64 columns, 128-byte swizzle, or of e4m3
 // codes in whole rows.
-int rows_map(const void *base, uint64_t rows, int D, int box_rows, bool q8, CUtensorMap *out) {
+int rows_map(const void *base, uint64_t rows, int D, int box_rows, bool q8, CUtensorMap *out,
+             CUtensorMapSwizzle q8_swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return LONGSPEC_HTA_ERR_CUDA;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
@@ -113,7 +114,7 @@ int rows_map(const void *base, uint64_t rows, int D, int box_rows, bool q8, CUte
     const cuuint32_t box[2] = {q8 ? static_cast<cuuint32_t>(D) : 64u, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
     return fn(out, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              q8 ? q8_swizzle : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
 }
@@ -138,8 +139,17 @@ int run_attention(hta::ChunkParams &p, const longspec_hta_dims *d, const longspe
     CUtensorMap tm[4] = {};
     const uint64_t cache_rows = 1ull * cache->num_blocks * d->Hkv * cache->block_size;
     const bool q8 = cache->k_scale != nullptr;
-    HTA_TRY(rows_map(cache->k_cache, cache_rows, d->D, cache->block_size, q8, &tm[0]));
-    HTA_TRY(rows_map(cache->v_cache, cache_rows, d->D, cache->block_size, q8, &tm[1]));
+    p.g_shift = 0;
+    while ((1 << p.g_shift) < p.G) ++p.g_shift;
+    p.g_mul = static_cast<uint32_t>((1ull << (31 + p.g_shift)) / p.G + 1);
+    // Few rows a sequence (16 packed ones on average at most) over an e4m3
+    // cache: the kernel for few rows.
+    const bool few = q8 && !p.tree && 1LL * d->T * p.G <= 16LL * d->B;
+    const CUtensorMapSwizzle sw = !few ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : d->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    HTA_TRY(rows_map(cache->k_cache, cache_rows, d->D, cache->block_size, q8, &tm[0], sw));
+    HTA_TRY(rows_map(cache->v_cache, cache_rows, d->D, cache->block_size, q8, &tm[1], sw));
+    if (few) return hta::launch_chunk_decode(p, tm, stream) == cudaSuccess ? LONGSPEC_HTA_OK : LONGSPEC_HTA_ERR_CUDA;
     if (p.tree_tiles) {
         const uint64_t rows = 1ull * d->B * d->Hkv * d->T;
         HTA_TRY(rows_map(p.k_tree, rows, d->D, 128, false, &tm[2]));

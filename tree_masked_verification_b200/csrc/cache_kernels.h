@@ -99,11 +99,12 @@ struct ChunkParams {
     __nv_bfloat16 *out;
     float *lse;
     uint32_t *status;
-    // schedule and partials (chunk_tc.cu): grid CTAs, two slots of slot_rows
+    // schedule and partials (chunk_plan.cuh): grid CTAs, two slots of slot_rows
     // rows each
     int grid, slot_rows;
     uint32_t g_mul;                   // division by G (div_g)
     int g_shift;
+    int item_rows;                    // packed rows of an item, at most
     int c0, c1, c2, min_share;        // units of work: an item, a key tile of one / two row tiles; least share of a CTA
     PartHead *heads;                  // [2 * grid]
     float *o_part, *lse_part;         // [2 * grid][slot_rows][D], [2 * grid][slot_rows]
@@ -112,6 +113,10 @@ struct ChunkParams {
 // columns by block_size rows with 128B swizzle, e4m3 in whole rows without;
 // K and V of the tree as [B*Hkv*N][D], box 64 x 128, 128B swizzle (not used
 // without tree tiles)
+// few rows of each sequence, e4m3 cache; K and V maps: whole rows of codes,
+// 128B (D = 128) or 64B (D = 64) swizzle
+cudaError_t launch_chunk_decode(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream);
 
 // -------------------------------------------------------------- device parts

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -92,12 +93,6 @@ class Cache(ctypes.Structure):
     _fields_ = PagedKV._fields_ + [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
-class Heads(ctypes.Structure):
-    """longspec_hta_heads: rows of heads at element strides (b, token, head)."""
-    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
-                ("stride_h", ctypes.c_int64)]
-
-
 class Rope(ctypes.Structure):
     """longspec_hta_rope: frequencies and norm weights of query and key heads."""
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
@@ -154,12 +149,13 @@ def load():
             lib.longspec_hta_window_workspace_bytes.argtypes = [pd]
             lib.longspec_hta_window_workspace_bytes.restype = sz
             lib.longspec_hta_commit_paged.argtypes = [pd, pk] + [vp] * 5 + [vp, sz, vp]
-            ph, pr, pc = ctypes.POINTER(Heads), ctypes.POINTER(Rope), ctypes.POINTER(Cache)
-            lib.longspec_hta_qk_norm_rope.argtypes = [ci] * 5 + [ph, ph, vp, pr, ph, ph, vp]
-            lib.longspec_hta_append_paged.argtypes = [pd, ph, ph, ph, pr, pc, vp, vp, ph, vp, sz, vp]
+            pr, pc = ctypes.POINTER(Rope), ctypes.POINTER(Cache)
+            # (longspec_hta_heads go over as packed bytes)
+            lib.longspec_hta_qk_norm_rope.argtypes = [ci] * 5 + [vp, vp, vp, pr, vp, vp, vp]
+            lib.longspec_hta_append_paged.argtypes = [pd, vp, vp, vp, pr, pc, vp, vp, vp, vp, sz, vp]
             lib.longspec_hta_chunk_workspace_bytes.argtypes = [pd]
             lib.longspec_hta_chunk_workspace_bytes.restype = sz
-            lib.longspec_hta_chunk_attention_paged.argtypes = [pd, ph, pc, vp, vp, ci] + [vp] * 3 + [sz, vp]
+            lib.longspec_hta_chunk_attention_paged.argtypes = [pd, vp, pc, vp, vp, ci] + [vp] * 3 + [sz, vp]
             lib.longspec_hta_q8_workspace_bytes.argtypes = [pd]
             lib.longspec_hta_q8_workspace_bytes.restype = sz
             lib.longspec_hta_verify_paged_q8.argtypes = [pd, vp, pc] + [vp] * 7 + [sz, vp]
@@ -321,23 +317,8 @@ def verify_paged(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, p
     new_q8_workspace(), and num_splits and prefix_events do not apply."""
     dev = q.device
     if k_scale is not None or v_scale is not None:
-        _no_prefix_options(num_splits, prefix_events)
-        for t, n in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree")):
-            _need(t, n, torch.bfloat16, dev)
-        _need(prefix_len, "prefix_len", torch.int32, dev)
-        _need(parent, "parent", torch.int32, dev)
-        cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
-        dims = _paged_dims(q, k_cache, L_cap, scale)
-        _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree, v_tree, parent)
-        st = _stream_on(dev, stream)
-        out = torch.empty_like(q) if out is None else _result(out, "out", q.shape, torch.bfloat16, dev)
-        lse = (torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None
-               else _result(lse, "lse", q.shape[:3], torch.float32, dev))
-        workspace = new_q8_workspace(dims, dev) if workspace is None else workspace
-        _check(load().longspec_hta_verify_paged_q8(
-            dims, q.data_ptr(), cache, prefix_len.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(),
-            parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
-        return out, lse
+        return _attention_q8(q, k_cache, v_cache, block_table, prefix_len, (k_tree, v_tree, parent), L_cap, out, lse,
+                             workspace, scale, num_splits, prefix_events, stream, k_scale, v_scale)
     for t, n in ((q, "q"), (k_tree, "k_tree"), (v_tree, "v_tree")):
         _need(t, n, torch.bfloat16, dev)
     _need(prefix_len, "prefix_len", torch.int32, dev)
@@ -365,21 +346,8 @@ def prefix_attention_paged(q, k_cache, v_cache, block_table, prefix_len, *, L_ca
     with k_scale and v_scale, in e4m3 (as in verify_paged)."""
     dev = q.device
     if k_scale is not None or v_scale is not None:
-        _no_prefix_options(num_splits, prefix_events)
-        _need(q, "q", torch.bfloat16, dev)
-        _need(prefix_len, "prefix_len", torch.int32, dev)
-        cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
-        dims = _paged_dims(q, k_cache, L_cap, scale)
-        _tree_shapes(dims, k_cache, prefix_len, block_table)
-        st = _stream_on(dev, stream)
-        out = torch.empty_like(q) if out is None else _result(out, "out", q.shape, torch.bfloat16, dev)
-        lse = (torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None
-               else _result(lse, "lse", q.shape[:3], torch.float32, dev))
-        workspace = new_q8_workspace(dims, dev) if workspace is None else workspace
-        _check(load().longspec_hta_prefix_attention_paged_q8(
-            dims, q.data_ptr(), cache, prefix_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), workspace.nbytes, st))
-        return out, lse
+        return _attention_q8(q, k_cache, v_cache, block_table, prefix_len, None, L_cap, out, lse, workspace, scale,
+                             num_splits, prefix_events, stream, k_scale, v_scale)
     _need(q, "q", torch.bfloat16, dev)
     _need(prefix_len, "prefix_len", torch.int32, dev)
     kv = _paged(k_cache, v_cache, block_table, dev)
@@ -576,22 +544,20 @@ def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, acce
     or, with k_scale and v_scale, in e4m3 (the rows are then stored as
     append_paged stores them)."""
     if k_scale is not None or v_scale is not None:
-        dev = k_tree.device
-        _need(k_tree, "k_tree", torch.bfloat16, dev)
-        _need(v_tree, "v_tree", torch.bfloat16, dev)
-        for t, n in ((prefix_len, "prefix_len"), (accept_len, "accept_len"), (path, "path")):
-            _need(t, n, torch.int32, dev)
+        dev = k_tree.get_device()
+        ptrs = [_flat(t, n, _BF16, dev) for t, n in ((k_tree, "k_tree"), (v_tree, "v_tree"))]
+        ptrs += [_flat(t, n, _I32, dev) for t, n in ((accept_len, "accept_len"), (path, "path"))]
+        pre = _flat(prefix_len, "prefix_len", _I32, dev)
         cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
         dims = _commit_dims(k_tree, L_cap)
         _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree, v_tree, path)
-        if tuple(accept_len.shape) != (dims.B,):
+        if accept_len.shape != (dims.B,):
             raise ValueError(f"accept_len must be [{dims.B}]")
         st = _stream_on(dev, stream)
         if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+            workspace = torch.zeros(256, dtype=torch.uint8, device=k_tree.device)
         _check(load().longspec_hta_commit_paged_q8(
-            dims, cache, prefix_len.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), accept_len.data_ptr(),
-            path.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
+            dims, cache, pre, *ptrs, _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
         return
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_tree, "k_tree"), (v_tree, "v_tree")):
         _need(t, n, torch.bfloat16, k_tree.device)
@@ -609,45 +575,60 @@ def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, acce
 
 # ---- new tokens: norm, rotation, append, chunk attention; the e4m3 cache ----
 
-def _stream_on(dev, stream) -> int:
+# These calls are short on the device, so the binding keeps its own time
+# short: device indices are compared as ints, row descriptors are packed bytes,
+# the current stream is read as the raw handle.
+
+_BF16, _I32 = torch.bfloat16, torch.int32
+_heads_struct = struct.Struct("4q").pack          # longspec_hta_heads
+_contiguous = torch.contiguous_format
+
+
+def _stream_on(dev: int, stream) -> int:
     """The stream to launch on; the tensors must be on the current device."""
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, which is not the current CUDA device")
-    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev.index:
-        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors are on {dev}")
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors are on cuda:{dev}")
     return _stream(stream)
 
 
-def _result(t, name, shape, dtype, dev):
-    _need(t, name, dtype, dev)
+def _flat(t, name, dtype, dev: int):
+    """A contiguous tensor's pointer."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _result(t, name, shape, dtype, dev: int):
+    _flat(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
-def _no_prefix_options(num_splits, prefix_events):
-    if num_splits or prefix_events:
-        raise ValueError("num_splits and prefix_events do not apply to an e4m3 cache")
-
-
-def _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev) -> Cache:
-    dtype = torch.bfloat16
+def _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev: int) -> Cache:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or block_table.dim() != 2:
+        raise ValueError("k/v_cache must be [num_blocks][Hkv][block_size][D], block_table [B][max_blocks]")
+    dtype, ks, vs = _BF16, None, None
     if k_scale is not None or v_scale is not None:
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache has both k_scale and v_scale")
         dtype = torch.float8_e4m3fn
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need(t, n, torch.uint8, dev)
-            if t.shape != k_cache.shape[:3]:
-                raise ValueError(f"{n} must be [num_blocks][Hkv][block_size]")
-    _need(k_cache, "k_cache", dtype, dev)
-    _need(v_cache, "v_cache", dtype, dev)
-    _need(block_table, "block_table", torch.int32, dev)
-    shape = k_cache.shape
-    if len(shape) != 4 or shape != v_cache.shape or block_table.dim() != 2:
-        raise ValueError("k/v_cache must be [num_blocks][Hkv][block_size][D], block_table [B][max_blocks]")
-    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), shape[0], shape[2],
-                 block_table.shape[1], _ptr(k_scale), _ptr(v_scale))
+        ks, vs = _flat(k_scale, "k_scale", torch.uint8, dev), _flat(v_scale, "v_scale", torch.uint8, dev)
+        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+            raise ValueError("k_scale and v_scale must be [num_blocks][Hkv][block_size]")
+    return Cache(_flat(k_cache, "k_cache", dtype, dev), _flat(v_cache, "v_cache", dtype, dev),
+                 _flat(block_table, "block_table", _I32, dev), shape[0], shape[2], block_table.shape[1], ks, vs)
 
 
 def _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree=None, v_tree=None, nodes=None):
@@ -661,36 +642,35 @@ def _tree_shapes(dims, k_cache, prefix_len, block_table, k_tree=None, v_tree=Non
                          f"[{dims.B}][{dims.T}]")
 
 
-def _heads(t, name, dev, axes):
-    """Heads of a bf16 tensor whose rows are D contiguous values; axes: its
-    strides' places for (b, token, head), None for no batch axis."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+def _heads(t, name, dev: int, b, n, h):
+    """longspec_hta_heads of a bf16 tensor whose rows are D contiguous values;
+    b, n, h: its axes (batch, token, head), b -1 for none."""
+    if t.dtype != _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    b, n, h = axes
-    return Heads(t.data_ptr(), 0 if b is None else st[b], st[n], st[h])
+    return _heads_struct(t.data_ptr(), 0 if b < 0 else st[b], st[n], st[h])
 
 
-_TOKENS, _BATCHED = (None, 0, 1), (0, 2, 1)     # [N][H][D] and [B][H][T][D]
-
-
-def _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev) -> Rope:
-    _need(inv_freq, "inv_freq", torch.float32, dev)
+def _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev: int) -> Rope:
+    f = _flat(inv_freq, "inv_freq", torch.float32, dev)
     if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
         raise ValueError(f"inv_freq must be [rot_dim / 2] with rot_dim from 2 to {D}")
     if not rope_scale > 0:
         raise ValueError("rope_scale must be above 0")
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, n, torch.bfloat16, dev)
-            if w.shape != (D,):
-                raise ValueError(f"{n} must be [{D}]")
-    return Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, _ptr(q_weight),
-                _ptr(k_weight), eps)
+    qw = kw = None
+    if q_weight is not None:
+        qw = _flat(q_weight, "q_weight", _BF16, dev)
+        if q_weight.shape != (D,):
+            raise ValueError(f"q_weight must be [{D}]")
+    if k_weight is not None:
+        kw = _flat(k_weight, "k_weight", _BF16, dev)
+        if k_weight.shape != (D,):
+            raise ValueError(f"k_weight must be [{D}]")
+    return Rope(f, 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale, qw, kw, eps)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -706,71 +686,68 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     frequencies and, as rope_scale, the factor on cos and sin that goes with
     them.  Returns (q_out, k_out), contiguous unless given; q_out=q, k_out=k
     works in place."""
-    dev = q.device
-    if q.dim() != k.dim() or q.dim() not in (3, 4):
-        raise ValueError("q and k must be [N][H][D] or [B][H][T][D]")
-    axes = _TOKENS if q.dim() == 3 else _BATCHED
-    shape, ks = q.shape, k.shape
-    if q.dim() == 3:
-        B, T, Hq, Hkv, D = 1, shape[0], shape[1], ks[1], shape[2]
+    dev, shape, ks = q.get_device(), q.shape, k.shape
+    if len(shape) == 3 and len(ks) == 3:
+        (T, Hq, D), B, Hkv, b, n, h = shape, 1, ks[1], -1, 0, 1
         same, want = ks[0] == T, (T,)
-    else:
-        B, T, Hq, Hkv, D = shape[0], shape[2], shape[1], ks[1], shape[3]
+    elif len(shape) == 4 and len(ks) == 4:
+        (B, Hq, T, D), Hkv, b, n, h = shape, ks[1], 0, 2, 1
         same, want = ks[0] == B and ks[2] == T, (B, T)
+    else:
+        raise ValueError("q and k must be [N][H][D] or [B][H][T][D]")
     if not same or ks[-1] != D:
         raise ValueError(f"q {list(shape)} and k {list(ks)} do not belong together")
-    _need(positions, "positions", torch.int32, dev)
+    pos = _flat(positions, "positions", _I32, dev)
     if positions.shape != want:
         raise ValueError(f"positions must be {list(want)}, got {list(positions.shape)}")
     rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev)
     st = _stream_on(dev, stream)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty_like(q, memory_format=_contiguous)
     elif q_out.shape != shape:
         raise ValueError(f"q_out must be {list(shape)}")
     if k_out is None:
-        k_out = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty_like(k, memory_format=_contiguous)
     elif k_out.shape != ks:
         raise ValueError(f"k_out must be {list(ks)}")
-    _check(load().longspec_hta_qk_norm_rope(
-        B, T, Hq, Hkv, D, _heads(q, "q", dev, axes), _heads(k, "k", dev, axes), positions.data_ptr(), rope,
-        _heads(q_out, "q_out", dev, axes), _heads(k_out, "k_out", dev, axes), st))
+    _check((_lib or load()).longspec_hta_qk_norm_rope(
+        B, T, Hq, Hkv, D, _heads(q, "q", dev, b, n, h), _heads(k, "k", dev, b, n, h), pos, rope,
+        _heads(q_out, "q_out", dev, b, n, h), _heads(k_out, "k_out", dev, b, n, h), st))
     return q_out, k_out
 
 
-def _ragged(prefix_len, q_start, block_table, dev):
-    _need(prefix_len, "prefix_len", torch.int32, dev)
-    _need(q_start, "q_start", torch.int32, dev)
+def _ragged(prefix_len, q_start, block_table, dev: int):
+    pre, start = _flat(prefix_len, "prefix_len", _I32, dev), _flat(q_start, "q_start", _I32, dev)
     B = prefix_len.shape[0] if prefix_len.dim() == 1 else 0
     if B < 1 or q_start.shape != (B + 1,) or block_table.shape[0] != B:
         raise ValueError("prefix_len must be [B], q_start [B + 1], block_table [B][max_blocks]")
-    return B
+    return B, pre, start
 
 
 def _append(q, k, v, rope, k_cache, v_cache, block_table, prefix_len, q_start, L_cap, k_scale, v_scale, q_out,
             workspace, stream):
-    dev = k.device
+    dev = k.get_device()
     N, Hkv, D = k.shape
     if v.shape != k.shape or (q is not None and (q.dim() != 3 or q.shape[0] != N or q.shape[2] != D)):
         raise ValueError("k and v must be [N][Hkv][D], q [N][Hq][D]")
     if k_cache.dim() != 4 or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
         raise ValueError(f"the cache must be [num_blocks][{Hkv}][block_size][{D}]")
     cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
-    B = _ragged(prefix_len, q_start, block_table, dev)
+    B, pre, start = _ragged(prefix_len, q_start, block_table, dev)
     st = _stream_on(dev, stream)
-    qh = oh = None
+    Hq, qh, oh = Hkv, None, None
     if q is not None:
+        Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty_like(q, memory_format=_contiguous)
         elif q_out.shape != q.shape:
             raise ValueError(f"q_out must be {list(q.shape)}")
-        qh, oh = _heads(q, "q", dev, _TOKENS), _heads(q_out, "q_out", dev, _TOKENS)
+        qh, oh = _heads(q, "q", dev, -1, 0, 1), _heads(q_out, "q_out", dev, -1, 0, 1)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
-    _check(load().longspec_hta_append_paged(
-        Dims(B, Hkv if q is None else q.shape[1], Hkv, D, N, L_cap, 0.0), qh, _heads(k, "k", dev, _TOKENS),
-        _heads(v, "v", dev, _TOKENS), rope, cache, prefix_len.data_ptr(), q_start.data_ptr(), oh,
-        workspace.data_ptr(), workspace.nbytes, st))
+        workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
+    _check((_lib or load()).longspec_hta_append_paged(
+        Dims(B, Hq, Hkv, D, N, L_cap, 0.0), qh, _heads(k, "k", dev, -1, 0, 1), _heads(v, "v", dev, -1, 0, 1), rope,
+        cache, pre, start, oh, _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
     return q_out
 
 
@@ -802,7 +779,7 @@ def rope_append_paged(q, k, v, inv_freq, k_cache, v_cache, block_table, prefix_l
     pass: q and k are normed and rotated at their positions
     prefix_len[b] + place in the chunk, k and v go to the cache.  Returns
     q_out [N][Hq][D]; padding rows of it are left as they were."""
-    rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, k.shape[-1], k.device)
+    rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, k.shape[-1], k.get_device())
     return _append(q, k, v, rope, k_cache, v_cache, block_table, prefix_len, q_start, L_cap, k_scale, v_scale, q_out,
                    workspace, stream)
 
@@ -829,25 +806,51 @@ def chunk_attention_paged(q, k_cache, v_cache, block_table, prefix_len, q_start,
     mixtures are all such chunks.  The cache is bf16, or e4m3 with scales.
     Returns (out bf16 [N][Hq][D], lse fp32 [N][Hq]); padding rows (from
     q_start[B] on) are left as they were."""
-    dev = q.device
-    N, Hq, D = q.shape
+    dev = q.get_device()
+    N, Hq, D = shape = q.shape
     if k_cache.dim() != 4 or k_cache.shape[3] != D or Hq % k_cache.shape[1]:
         raise ValueError(f"the cache must be [num_blocks][Hkv][block_size][{D}] with Hkv dividing {Hq}")
     cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
-    B = _ragged(prefix_len, q_start, block_table, dev)
+    B, pre, start = _ragged(prefix_len, q_start, block_table, dev)
     st = _stream_on(dev, stream)
-    qh = _heads(q, "q", dev, _TOKENS)
-    if qh.stride_h != D:
+    if q.stride(1) != D:
         raise ValueError("q: the heads of a token must be contiguous")
-    out = (torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev) if out is None
-           else _result(out, "out", (N, Hq, D), torch.bfloat16, dev))
-    lse = (torch.empty((N, Hq), dtype=torch.float32, device=dev) if lse is None
+    out = torch.empty_like(q, memory_format=_contiguous) if out is None else _result(out, "out", shape, _BF16, dev)
+    lse = (q.new_empty((N, Hq), dtype=torch.float32) if lse is None
            else _result(lse, "lse", (N, Hq), torch.float32, dev))
     if workspace is None:
         workspace = new_chunk_workspace(q, k_cache, B, L_cap=L_cap)
-    _check(load().longspec_hta_chunk_attention_paged(
-        Dims(B, Hq, k_cache.shape[1], D, N, L_cap, scale), qh, cache, prefix_len.data_ptr(), q_start.data_ptr(),
-        window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, st))
+    _check((_lib or load()).longspec_hta_chunk_attention_paged(
+        Dims(B, Hq, k_cache.shape[1], D, N, L_cap, scale), _heads(q, "q", dev, -1, 0, 1), cache, pre, start, window,
+        out.data_ptr(), lse.data_ptr(), _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
+    return out, lse
+
+
+def _attention_q8(q, k_cache, v_cache, block_table, prefix_len, tree, L_cap, out, lse, workspace, scale, num_splits,
+                  prefix_events, stream, k_scale, v_scale):
+    """verify_paged (tree: k_tree, v_tree, parent) or prefix_attention_paged
+    over an e4m3 cache."""
+    if num_splits or prefix_events:
+        raise ValueError("num_splits and prefix_events do not apply to an e4m3 cache")
+    dev, shape = q.get_device(), q.shape
+    qp, pre = _flat(q, "q", _BF16, dev), _flat(prefix_len, "prefix_len", _I32, dev)
+    cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
+    dims = _paged_dims(q, k_cache, L_cap, scale)
+    kt, vt, parent = tree or (None, None, None)
+    _tree_shapes(dims, k_cache, prefix_len, block_table, kt, vt, parent)
+    st = _stream_on(dev, stream)
+    out = torch.empty_like(q) if out is None else _result(out, "out", shape, _BF16, dev)
+    lse = (q.new_empty(shape[:3], dtype=torch.float32) if lse is None
+           else _result(lse, "lse", shape[:3], torch.float32, dev))
+    workspace = new_q8_workspace(dims, q.device) if workspace is None else workspace
+    end = (out.data_ptr(), lse.data_ptr(), _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st)
+    lib = _lib or load()
+    if tree is None:
+        _check(lib.longspec_hta_prefix_attention_paged_q8(dims, qp, cache, pre, *end))
+    else:
+        _check(lib.longspec_hta_verify_paged_q8(dims, qp, cache, pre, _flat(kt, "k_tree", _BF16, dev),
+                                                _flat(vt, "v_tree", _BF16, dev), _flat(parent, "parent", _I32, dev),
+                                                *end))
     return out, lse
 
 
