@@ -13,9 +13,11 @@
 //
 // One CTA per SM takes its range of the schedule (chunk_plan.cuh, items of
 // up to 16 rows).  A producer warp keeps four 128-key stages of codes and
-// scale bytes on their way by TMA; eight warps each take 16 keys of every
-// tile with a running maximum, sum and output of their own, joined once per
-// item.  Fragments without transposing loads: the contraction order of an
+// scale bytes on their way by TMA; four warps take the even tiles and four the
+// odd ones, 32 keys each, every warp with a running maximum, sum and output
+// of its own, joined once per item.  (16 keys of every tile a warp took 158
+// us for 256k keys: the chain from the codes to the second product is a
+// latency, and two key groups in it hide each other's.)  Fragments without transposing loads: the contraction order of an
 // MMA is free as long as both operands follow it, so a lane's four bytes of
 // K stand for the four d its A fragment (Q) holds, and for V a lane loads 16
 // bytes of four keys and pairs the bytes of neighbouring keys itself.
@@ -100,7 +102,7 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, kDecWarps); }
+        for (int i = 0; i < C::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, kDecWarps / 2); }
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -217,59 +219,51 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
-        for (int j = w.j0; j < w.j1; ++j) {
+        float f[2] = {1.f, 1.f};                        // 2^(m - M)
+        for (int j = w.j0; j < w.j1; ++j, st = st + 1 == C::NS ? 0 : st + 1, ph ^= st == 0 ? 1 : 0) {
+            if (((j - w.j0) & 1) != (warp >> 2)) continue;
             if (ok) ok = warp_wait(full + st, ph);
             const uint8_t *ks = smem + C::OFF_STAGE + st * 2 * C::RAW, *vs = ks + C::RAW;
             const uint8_t *sc = smem + C::OFF_SCALE + st * 256;
-            const int r0 = warp * 16;
-            // ---- scores of 16 rows x 16 keys: key r0 + 8u + 2t (+1), rows g (values 0, 1) and g + 8 (2, 3)
-            float x[2][4];
+            const int r0 = (warp & 3) * 32;
+            // ---- scores of 16 rows x 32 keys: key r0 + 8u + 2t (+1), rows g (values 0, 1) and g + 8 (2, 3)
+            float x[4][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
+            for (int u = 0; u < 4; ++u) x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
 #pragma unroll
-                for (int i = 0; i < KI; ++i) {
-                    const uint4 c = *reinterpret_cast<const uint4 *>(ks + piece<D>(r0 + 8 * u + g, KI * t + i));
-                    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+            for (int i = 0; i < KI; ++i) {
+                uint4 c[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma16816(x[u], qf[i * 4 + k], e4m3x2_to_f16x2(cw[k]), e4m3x2_to_f16x2(cw[k] >> 16));
-                }
+                for (int u = 0; u < 4; ++u) c[u] = *reinterpret_cast<const uint4 *>(ks + piece<D>(r0 + 8 * u + g, KI * t + i));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t cw = k == 0 ? c[u].x : k == 1 ? c[u].y : k == 2 ? c[u].z : c[u].w;
+                        mma16816(x[u], qf[i * 4 + k], e4m3x2_to_f16x2(cw), e4m3x2_to_f16x2(cw >> 16));
+                    }
             }
-            // ---- V codes of keys r0 + 2t, +1, +8, +9: the lane's D/8 columns
-            uint32_t vc[4][D / 32];
+            // ---- scales: bytes of the lane's eight keys, K's as 2^(e - 127), V's as bytes
+            int ev[8];
+            bool nan_key = false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = r0 + 2 * t + (k & 1) + 8 * (k >> 1);
-                if constexpr (D == 128) {
-                    const uint4 c = *reinterpret_cast<const uint4 *>(vs + piece<D>(r, g));
-                    vc[k][0] = c.x; vc[k][1] = c.y; vc[k][2] = c.z; vc[k][3] = c.w;
-                } else {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(vs + piece<D>(r, g >> 1) + (g & 1) * 8);
-                    vc[k][0] = c.x; vc[k][1] = c.y;
-                }
-            }
-            // ---- scales: bytes of the lane's four keys (u = key >> 3)
-            int ek[4], ev[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 4; ++u) {
                 const uint32_t a = *reinterpret_cast<const uint16_t *>(sc + r0 + 8 * u + 2 * t);
                 const uint32_t b = *reinterpret_cast<const uint16_t *>(sc + 128 + r0 + 8 * u + 2 * t);
-                ek[2 * u] = a & 255; ek[2 * u + 1] = a >> 8;
-                ev[2 * u] = b & 255; ev[2 * u + 1] = b >> 8;
+                ev[2 * u] = b & 255;
+                ev[2 * u + 1] = b >> 8;
+                nan_key |= ev[2 * u] == kScaleNan || ev[2 * u + 1] == kScaleNan;
+                const float s0 = __uint_as_float((a & 255) << 23), s1 = __uint_as_float((a >> 8) << 23);
+                x[u][0] *= qs[0] * s0;
+                x[u][1] *= qs[0] * s1;
+                x[u][2] *= qs[1] * s0;
+                x[u][3] *= qs[1] * s1;
             }
+            uint32_t dead = 0;                          // V rows (bit per key of the lane) to be read as zeros
+            if (__any_sync(0xffffffffu, nan_key) || w.partial(j)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float s = __uint_as_float(static_cast<uint32_t>(ek[k]) << 23);
-                x[k >> 1][k & 1] *= qs[0] * s;
-                x[k >> 1][2 + (k & 1)] *= qs[1] * s;
-            }
-            const bool masked = w.partial(j);
-            const bool some_nan = __any_sync(0xffffffffu, ev[0] == kScaleNan || ev[1] == kScaleNan || ev[2] == kScaleNan || ev[3] == kScaleNan);
-            if (masked || some_nan) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = w.key0(j) + r0 + 2 * t + (k & 1) + 8 * (k >> 1);
+                for (int k = 0; k < 8; ++k) {
+                    const int key = w.key0(j) + r0 + 8 * (k >> 1) + 2 * t + (k & 1);
                     const bool live = key >= w.it.lo && key < w.it.hi;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -280,45 +274,51 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     // what no row may see, or holds NaN, must not meet a weight of 0
                     if (!live || ev[k] == kScaleNan) {
                         ev[k] = 127;
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i) vc[k][i] = 0;
+                        dead |= 1u << k;
                     }
                 }
                 __syncwarp();
             }
             // ---- weights
-            uint32_t a[4];
+            uint32_t a[2][4];
             float M_up[2] = {1.f, 1.f};
             bool grew = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float xv[4], mt = -INFINITY, Mt = -INFINITY, y[4];
+                float mt = -INFINITY, Mt = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    xv[k] = x[k >> 1][2 * r + (k & 1)];
-                    y[k] = xv[k] + static_cast<float>(ev[k] - 127);
-                    mt = fmaxf(mt, xv[k]);
-                    Mt = fmaxf(Mt, y[k]);
+                for (int k = 0; k < 8; ++k) {
+                    const float xv = x[k >> 1][2 * r + (k & 1)];
+                    mt = fmaxf(mt, xv);
+                    // (2^23 + e) - (2^23 + 127), the conversion without the slow unit
+                    Mt = fmaxf(Mt, xv + (__uint_as_float(0x4b000000u | ev[k]) - 8388735.f));
                 }
                 mt = quad_max(mt);
                 Mt = quad_max(Mt);
-                if (mt > m[r] + 8.f) {
-                    l[r] *= ex2(m[r] - mt);
-                    m[r] = mt;
+                if (mt > m[r] + 8.f || Mt > M[r] + 8.f) {
+                    if (mt > m[r] + 8.f) {
+                        l[r] *= ex2(m[r] - mt);
+                        m[r] = mt;
+                    }
+                    if (Mt > M[r] + 8.f) {
+                        M_up[r] = ex2(M[r] - Mt);
+                        M[r] = Mt;
+                        grew = true;
+                    }
+                    f[r] = ex2(m[r] - M[r]);
                 }
-                if (Mt > M[r] + 8.f) {
-                    M_up[r] = ex2(M[r] - Mt);
-                    M[r] = Mt;
-                    grew = true;
-                }
-                const float mu = m[r] == -INFINITY ? 0.f : m[r], Mu = M[r] == -INFINITY ? 0.f : M[r];
+                const float mu = m[r] == -INFINITY ? 0.f : m[r];
+                float y[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    l[r] += ex2(xv[k] - mu);
-                    y[k] = ex2(y[k] - Mu);
+                for (int k = 0; k < 8; ++k) {
+                    const float w1 = ex2(x[k >> 1][2 * r + (k & 1)] - mu);
+                    l[r] += w1;
+                    y[k] = w1 * (__uint_as_float(static_cast<uint32_t>(ev[k]) << 23) * f[r]);
                 }
-                a[r] = pack_f16x2(y[0], y[1]);
-                a[2 + r] = pack_f16x2(y[2], y[3]);
+                a[0][r] = pack_f16x2(y[0], y[1]);
+                a[0][2 + r] = pack_f16x2(y[2], y[3]);
+                a[1][r] = pack_f16x2(y[4], y[5]);
+                a[1][2 + r] = pack_f16x2(y[6], y[7]);
             }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -327,19 +327,40 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     acc[i][2] *= M_up[1]; acc[i][3] *= M_up[1];
                 }
             }
-            // ---- O += P V; n8 tile i: column (D/8) * n + i
+            // ---- O += P V, 16 keys at a time; n8 tile i: column (D/8) * n + i
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t lo01 = __byte_perm(vc[0][i], vc[1][i], 0x5140), hi01 = __byte_perm(vc[0][i], vc[1][i], 0x7362);
-                const uint32_t lo23 = __byte_perm(vc[2][i], vc[3][i], 0x5140), hi23 = __byte_perm(vc[2][i], vc[3][i], 0x7362);
-                mma16816(acc[4 * i + 0], a, e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo23));
-                mma16816(acc[4 * i + 1], a, e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo23 >> 16));
-                mma16816(acc[4 * i + 2], a, e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi23));
-                mma16816(acc[4 * i + 3], a, e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi23 >> 16));
+            for (int h = 0; h < 2; ++h) {
+                uint32_t vc[4][D / 32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = r0 + 16 * h + 2 * t + (k & 1) + 8 * (k >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 c = *reinterpret_cast<const uint4 *>(vs + piece<D>(r, g));
+                        vc[k][0] = c.x; vc[k][1] = c.y; vc[k][2] = c.z; vc[k][3] = c.w;
+                    } else {
+                        const uint2 c = *reinterpret_cast<const uint2 *>(vs + piece<D>(r, g >> 1) + (g & 1) * 8);
+                        vc[k][0] = c.x; vc[k][1] = c.y;
+                    }
+                }
+                if (__any_sync(0xffffffffu, dead)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+                            if ((dead >> (4 * h + k)) & 1u) vc[k][i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t lo01 = __byte_perm(vc[0][i], vc[1][i], 0x5140), hi01 = __byte_perm(vc[0][i], vc[1][i], 0x7362);
+                    const uint32_t lo23 = __byte_perm(vc[2][i], vc[3][i], 0x5140), hi23 = __byte_perm(vc[2][i], vc[3][i], 0x7362);
+                    mma16816(acc[4 * i + 0], a[h], e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo23));
+                    mma16816(acc[4 * i + 1], a[h], e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo23 >> 16));
+                    mma16816(acc[4 * i + 2], a[h], e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi23));
+                    mma16816(acc[4 * i + 3], a[h], e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi23 >> 16));
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + st);
-            if (++st == C::NS) { st = 0; ph ^= 1; }
         }
 
         // ---- the eight warps' parts joined: row by row, m = max m_i,
