@@ -7,20 +7,24 @@
 // padding here and need every code rewritten as bf16 in shared memory first
 // (chunk_tc.cu on one sequence of 256k keys: 218 us).  Here codes go from
 // shared memory to registers and become exact f16 pairs in one conversion
-// each (e4m3 values fit f16), the operands of 16-row warp-level MMAs; the
+// each (e4m3 values fit f16), the operands of warp-level MMAs; the
 // row scales, powers of two, are applied to the scores and to the weights,
 // of which there are D times fewer.
 //
 // One CTA per SM takes its range of the schedule (chunk_plan.cuh, items of
-// up to 16 rows).  A producer warp keeps four 128-key stages of codes and
-// scale bytes on their way by TMA; four warps take the even tiles and four the
-// odd ones, 32 keys each, every warp with a running maximum, sum and output
-// of its own, joined once per item.  (16 keys of every tile a warp took 158
-// us for 256k keys: the chain from the codes to the second product is a
-// latency, and two key groups in it hide each other's.)  Fragments without transposing loads: the contraction order of an
-// MMA is free as long as both operands follow it, so a lane's four bytes of
-// K stand for the four d its A fragment (Q) holds, and for V a lane loads 16
-// bytes of four keys and pairs the bytes of neighbouring keys itself.
+// up to 8 or 16 rows).  A producer warp keeps four or five 128-key stages of
+// codes and scale bytes on their way by TMA; four warps take the even tiles
+// and four the odd ones, 32 keys each, every warp with a running maximum, sum
+// and output of its own, joined once per item.
+//
+// Both products put the long side on the MMA's 16 (keys, then d) and the
+// query rows on its 8:  S^T = K Q^T,  O^T += V^T P^T.  With rows on the 16,
+// decode's four to eight rows left most of each MMA empty, and the warp-level
+// MMA, 18 cycles each, was two thirds busy (256k keys: 137 us).  Fragments
+// without transposing loads: the contraction order of an MMA is free as long
+// as both operands follow it, so a lane's four bytes of K stand for the four
+// d its fragment of Q holds, and for V a lane loads D/8 bytes of four keys and
+// pairs the bytes of neighbouring keys itself.  P^T is turned by movmatrix.
 //
 // Precision.  Q is scaled per row by a power of two into f16's range, which
 // holds bf16's 8 bits exactly down to 2^-28 of the row's maximum.  Weights
@@ -34,21 +38,21 @@ namespace hta {
 
 namespace {
 
-constexpr int kDecRows = 16;
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = (kDecWarps + 1) * 32;
 
-template <int D>
+template <int D, int NR>                                    // NR: groups of 8 rows
 struct DecCfg {
-    static constexpr int NS = D == 128 ? 4 : 8;             // stages
+    static constexpr int ROWS = 8 * NR;
+    static constexpr int NS = D == 64 ? 8 : NR == 1 ? 5 : 4;   // stages
     static constexpr int RAW = 128 * D;
     static constexpr int STAGE = 2 * RAW + 256;             // K, V, scale bytes of K and of V
     static constexpr int OFF_STAGE = 0;                     // (codes at multiples of 1024: NS * 2 * RAW first)
     static constexpr int OFF_SCALE = NS * 2 * RAW;
     static constexpr int ROW = D + 4;                       // floats of an output row in the join
     static constexpr int OFF_JOIN = OFF_SCALE + NS * 256;   // [warp][row][ROW]
-    static constexpr int OFF_STAT = OFF_JOIN + kDecWarps * kDecRows * ROW * 4;   // [warp][row][m, l, M, bad]
-    static constexpr int OFF_BAR = OFF_STAT + kDecWarps * kDecRows * 16;
+    static constexpr int OFF_STAT = OFF_JOIN + kDecWarps * ROWS * ROW * 4;   // [warp][row][m, l, M, bad]
+    static constexpr int OFF_BAR = OFF_STAT + kDecWarps * ROWS * 16;
     static constexpr int OFF_MISC = OFF_BAR + 2 * NS * 8;   // abort; Start
     static constexpr int SMEM = OFF_MISC + 64;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
@@ -77,9 +81,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// over the lanes of one t (lane % 4): the keys of a warp
+__device__ __forceinline__ float keys_max(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 // 16-byte piece of a row of codes as TMA's swizzle left it: 128-byte rows in
@@ -89,11 +100,11 @@ __device__ __forceinline__ uint32_t piece(int row, int c) {
     return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(kDecThreads, 1)
 chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ ChunkParams p) {
-    using C = DecCfg<D>;
+    using C = DecCfg<D, NR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -102,7 +113,7 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, kDecWarps / 2); }
+        for (int i = 0; i < C::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, kDecWarps); }
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -169,7 +180,7 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int g = lane >> 2, t = lane & 3;
     const float nan = __int_as_float(0x7fc00000);
     constexpr int KI = D / 64;                          // 16-byte pieces of a K row per lane
-    constexpr int NT = D / 8;                           // n8 tiles of the output
+    constexpr int MT = D / 16;                          // m16 tiles of the output
     float *join = reinterpret_cast<float *>(smem + C::OFF_JOIN);
     float4 *stat = reinterpret_cast<float4 *>(smem + C::OFF_STAT);
     int st = 0, ph = 0;
@@ -177,17 +188,14 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int head_first = -1, head_last = -1;
     while (w.next(p)) {
         if (w.s.bad && threadIdx.x == 0) raise_status(p.status, kStatusPrefixLenRange);
-        // ---- Q: rows g and g + 8, the lane's d = [D/4 * t, D/4 * (t + 1)), as f16 fragments
-        uint32_t qf[KI * 4][4];
-        float qs[2];
-        int row_lo[2], row_hi[2];
+        // ---- Q: row 8n + g, the lane's d = [D/4 * t, D/4 * (t + 1)), as f16 fragments
+        uint32_t qf[NR][KI * 4][2];
+        float up_of[NR];                                // scale * log2(e) * 2^-(the row's shift)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
+        for (int n = 0; n < NR; ++n) {
+            const int row = 8 * n + g;
             const bool valid = row < w.it.rows;
             const int pr = w.it.r0 + (valid ? row : 0), tok = div_g(p, pr);
-            row_hi[r] = w.s.bad ? 0 : w.s.L + tok + 1;
-            row_lo[r] = p.window > 0 ? max(0, row_hi[r] - p.window) : 0;
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 p.q + (w.s.s0 + tok) * p.q_stride + static_cast<size_t>(w.cur_kvh * p.G + pr - tok * p.G) * D + t * (D / 4));
             uint4 u[KI * 2];
@@ -204,32 +212,55 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             // largest magnitude into [2^14, 2^15)
             const int up = min(14 - (static_cast<int>(big >> 7) - 127), 100);
             const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-            qs[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            up_of[n] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
             for (int i = 0; i < KI * 2; ++i) {
                 const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)     // bf16 pair i*4+k of the lane: k-step (i*4+k)/2, half k&1
-                    qf[(i * 4 + k) / 2][r + 2 * (k & 1)] = pack_f16x2(bf16_lo(x[k]) * mul, bf16_hi(x[k]) * mul);
+                for (int k = 0; k < 4; ++k)             // pair i*4+k of the lane: k-step (i*4+k)/2, half k&1
+                    qf[n][(i * 4 + k) / 2][k & 1] = pack_f16x2(bf16_lo(x[k]) * mul, bf16_hi(x[k]) * mul);
             }
         }
-        float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        bool bad[2] = {w.s.bad, w.s.bad};
-        float acc[NT][4];
+        // ---- the rows of this lane's scores: 8n + 2t + r, index 2n + r
+        float qs[2 * NR], m[2 * NR], M[2 * NR], l[2 * NR], f[2 * NR];   // f = 2^(m - M)
+        int row_lo[2 * NR], row_hi[2 * NR];
+        bool bad[2 * NR];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        for (int i = 0; i < 2 * NR; ++i) {
+            const int row = 8 * (i >> 1) + 2 * t + (i & 1);
+            qs[i] = __shfl_sync(0xffffffffu, up_of[i >> 1], (2 * t + (i & 1)) * 4);
+            row_hi[i] = w.s.bad ? 0 : w.s.L + div_g(p, w.it.r0 + min(row, w.it.rows - 1)) + 1;
+            row_lo[i] = p.window > 0 ? max(0, row_hi[i] - p.window) : 0;
+            m[i] = M[i] = -INFINITY;
+            l[i] = 0.f;
+            f[i] = 1.f;
+            bad[i] = w.s.bad;
+        }
+        float acc[NR][MT][4];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
 
-        float f[2] = {1.f, 1.f};                        // 2^(m - M)
         for (int j = w.j0; j < w.j1; ++j, st = st + 1 == C::NS ? 0 : st + 1, ph ^= st == 0 ? 1 : 0) {
-            if (((j - w.j0) & 1) != (warp >> 2)) continue;
+            // Every warp sees every phase of a stage and gives it back, whether the
+            // tile is its own or not: a wait by parity that skipped a phase would
+            // take the one before the last for the one it waits for.
             if (ok) ok = warp_wait(full + st, ph);
+            if (((j - w.j0) & 1) != (warp >> 2)) {
+                if (lane == 0) mbar_arrive(empty + st);
+                continue;
+            }
             const uint8_t *ks = smem + C::OFF_STAGE + st * 2 * C::RAW, *vs = ks + C::RAW;
             const uint8_t *sc = smem + C::OFF_SCALE + st * 256;
             const int r0 = (warp & 3) * 32;
-            // ---- scores of 16 rows x 32 keys: key r0 + 8u + 2t (+1), rows g (values 0, 1) and g + 8 (2, 3)
-            float x[4][4];
+            // ---- scores of 32 keys: m16 tile h holds keys r0 + 16h + g (values 0, 1: rows 2t, 2t + 1)
+            //      and r0 + 16h + 8 + g (values 2, 3); u = 2h + (key + 8)
+            float x[NR][2][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) x[n][h][0] = x[n][h][1] = x[n][h][2] = x[n][h][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 uint4 c[4];
@@ -238,96 +269,99 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t cw = k == 0 ? c[u].x : k == 1 ? c[u].y : k == 2 ? c[u].z : c[u].w;
-                        mma16816(x[u], qf[i * 4 + k], e4m3x2_to_f16x2(cw), e4m3x2_to_f16x2(cw >> 16));
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 c0 = c[2 * h], c1 = c[2 * h + 1];
+                        const uint32_t w0 = k == 0 ? c0.x : k == 1 ? c0.y : k == 2 ? c0.z : c0.w;
+                        const uint32_t w1 = k == 0 ? c1.x : k == 1 ? c1.y : k == 2 ? c1.z : c1.w;
+                        const uint32_t a[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16),
+                                               e4m3x2_to_f16x2(w1 >> 16)};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma16816(x[n][h], a, qf[n][i * 4 + k][0], qf[n][i * 4 + k][1]);
                     }
             }
-            // ---- scales: bytes of the lane's eight keys, K's as 2^(e - 127), V's as bytes
-            int ev[8];
+            // ---- scales of the lane's four keys, K's as 2^(e - 127), V's as bytes
+            int ev[4];
             bool nan_key = false;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const uint32_t a = *reinterpret_cast<const uint16_t *>(sc + r0 + 8 * u + 2 * t);
-                const uint32_t b = *reinterpret_cast<const uint16_t *>(sc + 128 + r0 + 8 * u + 2 * t);
-                ev[2 * u] = b & 255;
-                ev[2 * u + 1] = b >> 8;
-                nan_key |= ev[2 * u] == kScaleNan || ev[2 * u + 1] == kScaleNan;
-                const float s0 = __uint_as_float((a & 255) << 23), s1 = __uint_as_float((a >> 8) << 23);
-                x[u][0] *= qs[0] * s0;
-                x[u][1] *= qs[0] * s1;
-                x[u][2] *= qs[1] * s0;
-                x[u][3] *= qs[1] * s1;
-            }
-            uint32_t dead = 0;                          // V rows (bit per key of the lane) to be read as zeros
-            if (__any_sync(0xffffffffu, nan_key) || w.partial(j)) {
+                const float s = __uint_as_float(static_cast<uint32_t>(sc[r0 + 8 * u + g]) << 23);
+                ev[u] = sc[128 + r0 + 8 * u + g];
+                nan_key |= ev[u] == kScaleNan;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int key = w.key0(j) + r0 + 8 * (k >> 1) + 2 * t + (k & 1);
+                for (int i = 0; i < 2 * NR; ++i) x[i >> 1][u >> 1][2 * (u & 1) + (i & 1)] *= qs[i] * s;
+            }
+            const bool special = __any_sync(0xffffffffu, nan_key) || w.partial(j);
+            if (special) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int key = w.key0(j) + r0 + 8 * u + g;
                     const bool live = key >= w.it.lo && key < w.it.hi;
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const bool see = live && key >= row_lo[r] && key < row_hi[r];
-                        if (!see) x[k >> 1][2 * r + (k & 1)] = -INFINITY;
-                        bad[r] |= see && ev[k] == kScaleNan;
+                    for (int i = 0; i < 2 * NR; ++i) {
+                        const bool see = live && key >= row_lo[i] && key < row_hi[i];
+                        if (!see) x[i >> 1][u >> 1][2 * (u & 1) + (i & 1)] = -INFINITY;
+                        bad[i] |= see && ev[u] == kScaleNan;
                     }
-                    // what no row may see, or holds NaN, must not meet a weight of 0
-                    if (!live || ev[k] == kScaleNan) {
-                        ev[k] = 127;
-                        dead |= 1u << k;
-                    }
+                    if (!live || ev[u] == kScaleNan) ev[u] = 127;
                 }
                 __syncwarp();
             }
-            // ---- weights
-            uint32_t a[2][4];
-            float M_up[2] = {1.f, 1.f};
+            // ---- weights, P^T turned into the second product's fragments
+            uint32_t pb[NR][2][2];
+            float M_up[2 * NR];
             bool grew = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int i = 0; i < 2 * NR; ++i) {
+                M_up[i] = 1.f;
                 float mt = -INFINITY, Mt = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float xv = x[k >> 1][2 * r + (k & 1)];
+                for (int u = 0; u < 4; ++u) {
+                    const float xv = x[i >> 1][u >> 1][2 * (u & 1) + (i & 1)];
                     mt = fmaxf(mt, xv);
-                    // (2^23 + e) - (2^23 + 127), the conversion without the slow unit
-                    Mt = fmaxf(Mt, xv + (__uint_as_float(0x4b000000u | ev[k]) - 8388735.f));
+                    // (2^23 + e) - (2^23 + 127): the conversion without the slow unit
+                    Mt = fmaxf(Mt, xv + (__uint_as_float(0x4b000000u | ev[u]) - 8388735.f));
                 }
-                mt = quad_max(mt);
-                Mt = quad_max(Mt);
-                if (mt > m[r] + 8.f || Mt > M[r] + 8.f) {
-                    if (mt > m[r] + 8.f) {
-                        l[r] *= ex2(m[r] - mt);
-                        m[r] = mt;
+                mt = keys_max(mt);
+                Mt = keys_max(Mt);
+                if (mt > m[i] + 8.f || Mt > M[i] + 8.f) {
+                    if (mt > m[i] + 8.f) {
+                        l[i] *= ex2(m[i] - mt);
+                        m[i] = mt;
                     }
-                    if (Mt > M[r] + 8.f) {
-                        M_up[r] = ex2(M[r] - Mt);
-                        M[r] = Mt;
+                    if (Mt > M[i] + 8.f) {
+                        M_up[i] = ex2(M[i] - Mt);
+                        M[i] = Mt;
                         grew = true;
                     }
-                    f[r] = ex2(m[r] - M[r]);
+                    f[i] = ex2(m[i] - M[i]);
                 }
-                const float mu = m[r] == -INFINITY ? 0.f : m[r];
-                float y[8];
+                const float mu = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float w1 = ex2(x[k >> 1][2 * r + (k & 1)] - mu);
-                    l[r] += w1;
-                    y[k] = w1 * (__uint_as_float(static_cast<uint32_t>(ev[k]) << 23) * f[r]);
+                for (int u = 0; u < 4; ++u) {
+                    float &xv = x[i >> 1][u >> 1][2 * (u & 1) + (i & 1)];
+                    const float w1 = ex2(xv - mu);
+                    l[i] += w1;
+                    xv = w1 * (__uint_as_float(static_cast<uint32_t>(ev[u]) << 23) * f[i]);
                 }
-                a[0][r] = pack_f16x2(y[0], y[1]);
-                a[0][2 + r] = pack_f16x2(y[2], y[3]);
-                a[1][r] = pack_f16x2(y[4], y[5]);
-                a[1][2 + r] = pack_f16x2(y[6], y[7]);
             }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    pb[n][h][0] = transpose8x8(pack_f16x2(x[n][h][0], x[n][h][1]));
+                    pb[n][h][1] = transpose8x8(pack_f16x2(x[n][h][2], x[n][h][3]));
+                }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    acc[i][0] *= M_up[0]; acc[i][1] *= M_up[0];
-                    acc[i][2] *= M_up[1]; acc[i][3] *= M_up[1];
-                }
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        acc[n][i][0] *= M_up[2 * n]; acc[n][i][1] *= M_up[2 * n + 1];
+                        acc[n][i][2] *= M_up[2 * n]; acc[n][i][3] *= M_up[2 * n + 1];
+                    }
             }
-            // ---- O += P V, 16 keys at a time; n8 tile i: column (D/8) * n + i
+            // ---- O^T += V^T P^T, 16 keys at a time: keys 2t, 2t + 1, 2t + 8, 2t + 9 of them, the lane's
+            //      columns (D/8) g + c; m16 tile i holds c = 2i (row g) and 2i + 1 (row g + 8)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t vc[4][D / 32];
@@ -341,22 +375,27 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         const uint2 c = *reinterpret_cast<const uint2 *>(vs + piece<D>(r, g >> 1) + (g & 1) * 8);
                         vc[k][0] = c.x; vc[k][1] = c.y;
                     }
-                }
-                if (__any_sync(0xffffffffu, dead)) {
+                    if (special) {
+                        // what no row may see, or holds NaN, must not meet a weight of 0
+                        const int key = w.key0(j) + r;
+                        if (key < w.it.lo || key >= w.it.hi || sc[128 + r] == kScaleNan)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-                            if ((dead >> (4 * h + k)) & 1u) vc[k][i] = 0;
+                            for (int i = 0; i < D / 32; ++i) vc[k][i] = 0;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     const uint32_t lo01 = __byte_perm(vc[0][i], vc[1][i], 0x5140), hi01 = __byte_perm(vc[0][i], vc[1][i], 0x7362);
                     const uint32_t lo23 = __byte_perm(vc[2][i], vc[3][i], 0x5140), hi23 = __byte_perm(vc[2][i], vc[3][i], 0x7362);
-                    mma16816(acc[4 * i + 0], a[h], e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo23));
-                    mma16816(acc[4 * i + 1], a[h], e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo23 >> 16));
-                    mma16816(acc[4 * i + 2], a[h], e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi23));
-                    mma16816(acc[4 * i + 3], a[h], e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi23 >> 16));
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo23),
+                                           e4m3x2_to_f16x2(lo23 >> 16)};
+                    const uint32_t b[4] = {e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi23),
+                                           e4m3x2_to_f16x2(hi23 >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        mma16816(acc[n][2 * i], a, pb[n][h][0], pb[n][h][1]);
+                        mma16816(acc[n][2 * i + 1], b, pb[n][h][0], pb[n][h][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -366,45 +405,44 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         // ---- the eight warps' parts joined: row by row, m = max m_i,
         //      l = sum l_i 2^(m_i - m), o = sum O_i 2^(M_i - m) / l
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            int b = bad[r] || !ok;
-            b |= __shfl_xor_sync(0xffffffffu, b, 1);
-            b |= __shfl_xor_sync(0xffffffffu, b, 2);
+        for (int i = 0; i < 2 * NR; ++i) {
+            const int n = i >> 1, row = 8 * n + 2 * t + (i & 1);
+            int b = bad[i] || !ok;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+                b |= __shfl_xor_sync(0xffffffffu, b, o);
+            }
             if (row < w.it.rows) {
-                float *dst = join + (warp * kDecRows + row) * C::ROW + t * (D / 4);
+                float *dst = join + (warp * C::ROWS + row) * C::ROW + g * (D / 8);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < NT; i += 4)
-                        *reinterpret_cast<float4 *>(dst + h * NT + i) =
-                            make_float4(acc[i][2 * r + h], acc[i + 1][2 * r + h], acc[i + 2][2 * r + h], acc[i + 3][2 * r + h]);
-                if (t == 0) stat[warp * kDecRows + row] = make_float4(m[r], l[r], M[r], b ? 1.f : 0.f);
+                for (int c = 0; c < MT; c += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * c) = make_float4(acc[n][c][i & 1], acc[n][c][2 + (i & 1)],
+                                                                           acc[n][c + 1][i & 1], acc[n][c + 1][2 + (i & 1)]);
+                if (g == 0) stat[warp * C::ROWS + row] = make_float4(m[i], l[i], M[i], b ? 1.f : 0.f);
             }
         }
         bar_sync(1, kDecWarps * 32);
         const bool whole = w.j0 == 0 && w.j1 == w.it.nt;
         const int which = w.j0 > 0 ? 0 : 1;
         {
-            constexpr int PER = D / 16;                 // values of a thread
-            const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * PER;
+            constexpr int TPR = 256 / C::ROWS, PER = D / TPR > 4 ? D / TPR : 4;   // threads of a row, values of a thread
+            const int row = threadIdx.x / (D / PER), col = threadIdx.x % (D / PER) * PER;
             if (row < w.it.rows) {
                 float ms = -INFINITY, ls = 0.f, o[PER];
                 bool nan_row = false;
 #pragma unroll
-                for (int i = 0; i < kDecWarps; ++i) ms = fmaxf(ms, stat[i * kDecRows + row].x);
+                for (int i = 0; i < kDecWarps; ++i) ms = fmaxf(ms, stat[i * C::ROWS + row].x);
 #pragma unroll
                 for (int k = 0; k < PER; ++k) o[k] = 0.f;
 #pragma unroll
                 for (int i = 0; i < kDecWarps; ++i) {
-                    const float4 s = stat[i * kDecRows + row];
+                    const float4 s = stat[i * C::ROWS + row];
                     nan_row |= s.w != 0.f || s.y != s.y;
                     if (s.x == -INFINITY) continue;     // the warp saw none of the row's keys
                     ls += s.y * ex2(s.x - ms);
                     const float f = ex2(s.z - ms);
-                    const float *src = join + (i * kDecRows + row) * C::ROW + col;
+                    const float *src = join + (i * C::ROWS + row) * C::ROW + col;
 #pragma unroll
                     for (int k = 0; k < PER; k += 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(src + k);
@@ -447,16 +485,16 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream) {
-    using C = DecCfg<D>;
+    using C = DecCfg<D, NR>;
     constexpr int kMaxDev = 64;
     static bool attr_set[kMaxDev] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDev || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+        e = cudaFuncSetAttribute(chunk_decode_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
     }
@@ -470,7 +508,7 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(kDecThreads);
     cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    e = cudaLaunchKernelEx(&cfg, chunk_decode_kernel<D>, tm[0], tm[1], p);
+    e = cudaLaunchKernelEx(&cfg, chunk_decode_kernel<D, NR>, tm[0], tm[1], p);
     return e != cudaSuccess ? e : launch_chunk_merge(p, stream);
 }
 
@@ -478,12 +516,16 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
 
 cudaError_t launch_chunk_decode(const ChunkParams &p0, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     ChunkParams p = p0;
-    p.item_rows = kDecRows;
-    p.slot_rows = p.slot_rows < kDecRows ? p.slot_rows : kDecRows;
+    // 8 rows at a time unless sequences have more on average (a second group
+    // of 8 shares the codes' loads and conversions)
+    const bool wide = 1LL * p.N * p.G > 8LL * p.B;
+    p.item_rows = wide ? 16 : 8;
+    p.slot_rows = p.slot_rows < p.item_rows ? p.slot_rows : p.item_rows;
     p.c0 = 4;
     p.c1 = p.c2 = 4;
     p.min_share = 8;
-    return p.D == 128 ? launch<128>(p, tm, stream) : launch<64>(p, tm, stream);
+    if (p.D == 128) return wide ? launch<128, 2>(p, tm, stream) : launch<128, 1>(p, tm, stream);
+    return wide ? launch<64, 2>(p, tm, stream) : launch<64, 1>(p, tm, stream);
 }
 
 }  // namespace hta
