@@ -52,6 +52,10 @@ namespace hta {
 namespace {
 
 constexpr int kPoisonRing = 8;
+#ifndef HTA_POLY
+#define HTA_POLY 4
+#endif
+constexpr int kPolyEvery = HTA_POLY;               // one exp2 pair in this many on the FMA pipe (0: none)
 
 template <int D, bool Q8>
 struct Cfg {
@@ -70,11 +74,11 @@ struct Cfg {
     static constexpr int NUM_BARS = 5 + 3 * NK + 3 * NV + 4;
     static constexpr int OFF_POISON = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // [kPoisonRing][4] words
     static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort; Start
-    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // int16 [kTMax] (trees)
-    static constexpr int OFF_SCALE = OFF_PARENT + kTMax * 2;         // per K stage: scale bytes of K and of V
-    static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 : 0); // walks of the softmax groups and the loaders
-    static constexpr int WALK_BYTES = 160;
-    static constexpr int SMEM = OFF_WALK + 2 * WALK_BYTES;
+    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // parent + 1 of each node, a byte (trees)
+    static constexpr int OFF_SCALE = OFF_PARENT + kTMax;             // per K stage: scale bytes of K and of V; per V stage: V's
+    static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 + NV * 128 : 0);   // walks: softmax groups, K and V loaders
+    static constexpr int WALK_BYTES = 128;
+    static constexpr int SMEM = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;
     static constexpr int SMEM_ALLOC = SMEM + 1024;          // slack to align the base to 1024
     static constexpr int OFF_XCH = TILE;                    // [2][2][128] floats, in the unused second Q tile
     static constexpr int OFF_PLAN = OFF_K;                  // int64 [kPlanUnits], before the first copy
@@ -137,6 +141,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+// registers of a tensor-memory load that has been waited for
+__device__ __forceinline__ void pin(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // NaN if any operand is (a NaN score must not get lost in the clamps below)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -191,7 +201,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
-    int16_t *s_parent = reinterpret_cast<int16_t *>(smem + C::OFF_PARENT);
+    uint8_t *s_parent = smem + C::OFF_PARENT;       // (parent + 1)
     uint8_t *s_scale = smem + C::OFF_SCALE;
 
     if (threadIdx.x == 0) {
@@ -200,8 +210,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         mbar_init(o_full, 1);
         mbar_init(o_empty, 8);
         // (one arrive per loader warp, by TMA or by the fixer)
-        for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 8 : 1); mbar_init(k_empty + i, 1); mbar_init(k_raw + i, 1); }
-        for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 8 : 1); mbar_init(v_empty + i, 1); mbar_init(v_raw + i, 1); }
+        for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 4 : 1); mbar_init(k_empty + i, 1); mbar_init(k_raw + i, 1); }
+        for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 4 : 1); mbar_init(v_empty + i, 1); mbar_init(v_raw + i, 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(s_full + i, 1); mbar_init(p_ready + i, 4); }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -267,7 +277,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 } else if (w.it.hi == 0) {              // nothing to read: a wholly masked tile
                     if (lane == 0) mbar_arrive(full + st);
                 } else {
-                    if (lane == 0) mbar_arrive_expect_tx(full + st, Q8 ? C::RAW + (is_k ? 256 : 0) : C::TILE);
+                    if (lane == 0) mbar_arrive_expect_tx(full + st, Q8 ? C::RAW + (is_k ? 256 : 128) : C::TILE);
                     __syncwarp();
                     if (lane < nb) {
                         int n = id;
@@ -278,10 +288,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         const int y = (n * p.Hkv + w.cur_kvh) << bsh;
                         if constexpr (Q8) {
                             tma_load_2d(stage + C::TILE - C::RAW + (lane << bsh) * D, map, full + st, 0, y);
-                            if (is_k) {                 // the scale bytes of both come with K
+                            if (is_k) {                 // (V's scale bytes too: see the K loaders)
                                 uint8_t *sc = s_scale + st * 256 + (lane << bsh);
                                 bulk_load(sc, p.cache.k_scale + y, bs, full + st);
                                 bulk_load(sc + 128, p.cache.v_scale + y, bs, full + st);
+                            } else {
+                                bulk_load(s_scale + C::NK * 256 + st * 128 + (lane << bsh), p.cache.v_scale + y, bs, full + st);
                             }
                         } else {
 #pragma unroll
@@ -421,122 +433,97 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (elect_one()) mma_commit(drain);         // all MMAs issued are done before TMEM is freed
         warp_wait(drain, 0);
     } else if (warp >= kWarpLoad) {
-        // -------------------------------------------- loaders (e4m3 cache)
+        // ------------- loaders (e4m3 cache): four warps for K, four for V
         if constexpr (Q8) {
             regs_dec<C::REGS_LOAD>();
             constexpr int LPR = D / 8;              // lanes per cache row (8 codes each)
             constexpr int RW = 32 / LPR;            // rows of a warp and round
-            constexpr int ROUNDS = 16 / RW;         // a warp has 16 rows of a tile
-            const int lw = warp - kWarpLoad, c = lane % LPR;
-            // row of (round, row in the round); rows of one round are 8 * RW apart from the next's,
-            // so a lane's place in the swizzle is the same in every round
-            auto row_of = [&](int i, int k) { return i * 8 * RW + lw * RW + k; };
-            const int row0 = row_of(0, lane / LPR);
-            const uint32_t raw_off = C::TILE - C::RAW + row0 * D + c * 8;
-            const uint32_t out_off = (c >> 3) * C::BOX + row0 * 128 + (((c & 7) ^ (row0 & 7)) << 4);
-            Walk &lwk = *reinterpret_cast<Walk *>(smem + C::OFF_WALK + C::WALK_BYTES);
-            volatile int *more = reinterpret_cast<volatile int *>(smem + C::OFF_WALK + 2 * C::WALK_BYTES - 4);
-            const bool first_thread = threadIdx.x == kWarpLoad * 32;
-            int kst = 0, kph = 0, vst = 0, vph = 0, pos = 0;
+            constexpr int BATCH = D == 128 ? 4 : 8;  // rounds of loads in flight (D = 64: all, see convert)
+            const bool is_v = warp >= kWarpLoad + 4;
+            const int lw = (warp - kWarpLoad) & 3, c = lane % LPR, set_bar = is_v ? 3 : 2;
+            // a warp has the rows lw * 32 ..; its lane's place in the swizzle
+            // alternates with the round where a round is not a multiple of 8 rows
+            const int row0 = lw * 32 + lane / LPR;
+            Walk &lwk = *reinterpret_cast<Walk *>(smem + C::OFF_WALK + (is_v ? 2 : 1) * C::WALK_BYTES);
+            volatile int *more = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(&lwk) + C::WALK_BYTES - 4);
+            const bool first_thread = lw == 0 && lane == 0;
+            const int ns = is_v ? C::NV : C::NK;
+            uint8_t *ring = smem + (is_v ? C::OFF_V : C::OFF_K);
+            uint64_t *raw = is_v ? v_raw : k_raw, *full = is_v ? v_full : k_full;
+            int st = 0, ph = 0, pos = 0;
             bool ok = true;
             if (first_thread) lwk.start(p, s_start);
-            // a stage's codes to bf16, in place; lane l < 16 holds the multiplier
-            // of row (l / RW, l % RW), 0 for rows that are no keys
+            // A stage's codes to bf16, in place; lane l holds the multiplier of row
+            // lw * 32 + l, 0 for rows that are no keys.  At D = 128 a row's codes lie
+            // where its own second half goes, so a warp needs no other's progress;
+            // at D = 64 they lie where other warps' rows go.
             auto convert = [&](uint8_t *stage, uint32_t mult) {
-                uint2 u[ROUNDS];
+                const uint8_t *src = stage + C::TILE - C::RAW + c * 8;
+                auto part = [&](int i0, bool sync) {
+                    uint2 u[BATCH];
 #pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) u[i] = *reinterpret_cast<const uint2 *>(stage + raw_off + i * 8 * RW * D);
-                bar_sync(2, 256);                   // all codes are in registers
+                    for (int i = 0; i < BATCH; ++i) u[i] = *reinterpret_cast<const uint2 *>(src + (row0 + (i0 + i) * RW) * D);
+                    if (sync) bar_sync(set_bar, 128);
+                    else __syncwarp();
 #pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    const uint32_t m = __shfl_sync(0xffffffffu, mult, i * RW + lane / LPR);
-                    const uint2 a = dequant_e4m3x4(u[i].x, m), b = dequant_e4m3x4(u[i].y, m);
-                    *reinterpret_cast<uint4 *>(stage + out_off + i * 8 * RW * 128) = make_uint4(a.x, a.y, b.x, b.y);
-                }
-            };
-            auto publish = [&](uint64_t *full) {
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int row = row0 + (i0 + i) * RW;
+                        const uint32_t m = __shfl_sync(0xffffffffu, mult, (i0 + i) * RW + lane / LPR);
+                        const uint2 a = dequant_e4m3x4(u[i].x, m), b = dequant_e4m3x4(u[i].y, m);
+                        *reinterpret_cast<uint4 *>(stage + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(a.x, a.y, b.x, b.y);
+                    }
+                };
+                static_assert(D == 128 || 32 / RW == BATCH, "one batch where rows overlap other warps'");
+#pragma unroll 1
+                for (int i = 0; i < 32 / RW; i += BATCH) part(i, D != 128);
             };
             for (;;) {
-                bar_sync(2, 256);
+                bar_sync(set_bar, 128);
                 if (first_thread) *more = lwk.next(p);
-                bar_sync(2, 256);
+                bar_sync(set_bar, 128);
                 if (!*more) break;
                 const int j0 = lwk.j0, j1 = lwk.j1, cache_tiles = lwk.it.cache_tiles;
                 const int lo = lwk.it.lo, hi = lwk.it.hi, base = lwk.it.base;
-                uint32_t v_mult = 0;
-                // fill order K0 K1 V0 K2 V1 ...
-                for (int j = j0; j <= j1; ++j) {
-                    if (j < j1) {
-                        const int at = (pos % kPoisonRing) * 4;
-                        uint8_t *stage = smem + C::OFF_K + kst * C::TILE;
-                        if (ok) ok = warp_wait(k_raw + kst, kph);
-                        if (j < cache_tiles) {
-                            const uint8_t *sc = s_scale + kst * 256;
-                            const int a = lo - (base + j * 128), z = hi - (base + j * 128);     // live rows [a, z)
-                            const int r = row_of((lane & 15) / RW, (lane & 15) % RW);
-                            const bool live = r >= a && r < z;
-                            const uint32_t k_mult = live ? e4m3_mult(sc[r]) : 0u;
-                            // V rows held as NaN are zeroed and told to the softmax groups
-                            const int ev = sc[128 + r];
-                            const uint32_t v_next = live && ev != kScaleNan ? e4m3_mult(ev) : 0u;
-                            const int r4 = (lw & 3) * 32 + lane;
-                            const uint32_t word = __ballot_sync(0xffffffffu, r4 >= a && r4 < z && sc[128 + r4] == kScaleNan);
-                            if (lw < 4 && lane == 0) s_poison[at + lw] = word;
-                            convert(stage, k_mult);
-                            publish(k_full + kst);
-                            if (j > j0) {           // (V of the tile before still needs its own)
-                                const uint32_t t = v_mult;
-                                v_mult = v_next;
-                                uint8_t *vs = smem + C::OFF_V + vst * C::TILE;
-                                if (ok) ok = warp_wait(v_raw + vst, vph);
-                                convert(vs, t);
-                                publish(v_full + vst);
-                                if (++vst == C::NV) { vst = 0; vph ^= 1; }
-                            } else {
-                                v_mult = v_next;
-                            }
-                        } else {
-                            publish(k_full + kst);  // (rows behind the tree are masked)
+                for (int j = j0; j < j1; ++j, ++pos) {
+                    uint8_t *stage = ring + st * C::TILE;
+                    if (ok) ok = warp_wait(raw + st, ph);
+                    uint32_t *word = s_poison + (pos % kPoisonRing) * 4 + lw;
+                    if (j < cache_tiles) {
+                        const int r = lw * 32 + lane, key = base + j * 128 + r;
+                        const bool live = key >= lo && key < hi;
+                        const uint8_t *sc = is_v ? s_scale + C::NK * 256 + st * 128 : s_scale + st * 256;
+                        const int e = sc[r];
+                        if (!is_v) {
+                            // V rows held as NaN are told to the softmax groups with K, before they read the scores
+                            const uint32_t nan = __ballot_sync(0xffffffffu, live && sc[128 + r] == kScaleNan);
+                            if (lane == 0) *word = nan;
                         }
-                        if (++kst == C::NK) { kst = 0; kph ^= 1; }
-                        ++pos;
-                        if (j < cache_tiles) continue;
-                    }
-                    if (j > j0) {                   // V of tile j - 1 where tile j is not a cache tile
-                        uint8_t *vs = smem + C::OFF_V + vst * C::TILE;
-                        if (ok) ok = warp_wait(v_raw + vst, vph);
-                        if (j - 1 < cache_tiles) {
-                            convert(vs, v_mult);
-                        } else {
-                            // tree rows: 16 a warp, two lanes a row; rows behind the tree are
-                            // zeroed, and so are rows with an infinity or a NaN, which are told
-                            // to the softmax groups (they wait for this tile)
-                            const int at = ((pos - (j < j1 ? 2 : 1)) % kPoisonRing) * 4;
-                            const int r = lw * 16 + (lane >> 1), live = min(128, p.N - (j - 1 - cache_tiles) * 128);
-                            uint8_t *rp = vs + r * 128;
-                            uint32_t big = 0;
-                            for (int x = lane & 1; x < D / 8; x += 2) {
-                                const uint4 u = *reinterpret_cast<const uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4));
-                                big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
-                                big = __vmaxu2(big, u.w & 0x7fff7fffu);
-                            }
-                            big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                            const bool inf = r < live && max(big & 0xffffu, big >> 16) >= 0x7f80u;
-                            if (r >= live || inf)
-                                for (int x = lane & 1; x < D / 8; x += 2)
-                                    *reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                            uint32_t half = 0;      // a bit per row of the warp
-                            const uint32_t bits = __ballot_sync(0xffffffffu, inf);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) half |= ((bits >> (2 * x)) & 1u) << x;
-                            if (lane == 0) reinterpret_cast<uint16_t *>(s_poison + at)[lw] = static_cast<uint16_t>(half);
+                        convert(stage, live && !(is_v && e == kScaleNan) ? e4m3_mult(e) : 0u);
+                    } else if (is_v) {
+                        // tree rows, one a lane: rows behind the tree are zeroed, and so are rows
+                        // with an infinity or a NaN, which are told to the softmax groups (they
+                        // wait for this tile).  K rows behind the tree are masked.
+                        const int r = lw * 32 + lane, live = min(128, p.N - (j - cache_tiles) * 128);
+                        uint8_t *rp = stage + r * 128;
+                        uint32_t big = 0;
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4));
+                            big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
+                            big = __vmaxu2(big, u.w & 0x7fff7fffu);
                         }
-                        publish(v_full + vst);
-                        if (++vst == C::NV) { vst = 0; vph ^= 1; }
+                        const bool inf = r < live && max(big & 0xffffu, big >> 16) >= 0x7f80u;
+                        if (r >= live || inf)
+                            for (int x = 0; x < D / 8; ++x)
+                                *reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t nan = __ballot_sync(0xffffffffu, inf);
+                        if (lane == 0) *word = nan;
                     }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + st);
+                    if (++st == ns) { st = 0; ph ^= 1; }
                 }
             }
         }
@@ -612,7 +599,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (i < p.N) {
                     const int up = p.parent[static_cast<size_t>(w.cur_b) * p.N + i];
                     bad = up < -1 || up >= i;
-                    s_parent[i] = static_cast<int16_t>(up);
+                    s_parent[i] = static_cast<uint8_t>(up + 1);
                 }
                 __syncwarp();
                 tree_bad = bar_or(1, 256, bad);
@@ -644,7 +631,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see[i] = 0;
                             // (parents lie below their nodes, so the walk ends)
-                            for (int node = tree_bad ? -1 : t; node >= 0; node = s_parent[node]) {
+                            for (int node = tree_bad ? -1 : t; node >= 0; node = s_parent[node] - 1) {
                                 const int d = node - first;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) see[i] |= (d >> 5) == i ? 1u << (d & 31) : 0u;
@@ -664,102 +651,73 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     } else if (Q8) {
                         if (bad_v.x | bad_v.y | bad_v.z | bad_v.w) row_nan = true;
                     }
-                    auto hide = [&](uint32_t (&sc)[32], int q) {
-                        if (masked) {
-                            const uint32_t ninf = __float_as_uint(-INFINITY);
+                    // Three short loops over the row's 128 scores, 32 at a time, from
+                    // tensor memory each time: the code stays small.  (Unrolled over all
+                    // 128 it was fetched, not issued, at the pace the five roles that
+                    // share a scheduler left: see the figures above.)
+                    if (masked) {
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t x[32];
+                            tmem_ld32(t_s + 32 * q, x);
+                            tmem_wait_ld();
+                            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) sc[i] = (see[q] >> i) & 1u ? sc[i] : ninf;
+                            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? x[i] : __float_as_uint(-INFINITY);
+                            tmem_st32(t_s + 32 * q, x);
                         }
-                    };
-                    auto max32 = [&](const uint32_t (&sc)[32]) {
-                        float a = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            a = max3(a, __uint_as_float(sc[i]), __uint_as_float(sc[i + 1]));
-                            b2 = max3(b2, __uint_as_float(sc[i + 2]), __uint_as_float(sc[i + 3]));
-                        }
-                        return max3(a, b2, -INFINITY);
-                    };
-                    // bf16 caches: the row's 128 scores stay in registers; e4m3: they
-                    // are read twice, which leaves the loaders their registers
-                    uint32_t r0[32], r1[32], r2[32], r3[32];
-                    float m_tile;
-                    if constexpr (!Q8) {
-                        tmem_ld32(t_s + 0, r0);
-                        tmem_ld32(t_s + 32, r1);
-                        tmem_ld32(t_s + 64, r2);
-                        tmem_ld32(t_s + 96, r3);
-                        tmem_wait_ld();
-                        hide(r0, 0);
-                        hide(r1, 1);
-                        hide(r2, 2);
-                        hide(r3, 3);
-                        m_tile = max3(max3(max32(r0), max32(r1), max32(r2)), max32(r3), -INFINITY) * c2;
-                    } else {
-                        tmem_ld32(t_s + 0, r0);
-                        tmem_ld32(t_s + 32, r1);
-                        tmem_wait_ld();
-                        hide(r0, 0);
-                        hide(r1, 1);
-                        m_tile = max3(max32(r0), max32(r1), -INFINITY);
-                        tmem_ld32(t_s + 64, r0);
-                        tmem_ld32(t_s + 96, r1);
-                        tmem_wait_ld();
-                        hide(r0, 2);
-                        hide(r1, 3);
-                        m_tile = max3(m_tile, max32(r0), max32(r1)) * c2;
+                        tmem_wait_st();
                     }
+                    float mt = -INFINITY;
+                    {
+                        uint32_t x[2][32];
+                        tmem_ld32(t_s, x[0]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tmem_wait_ld();
+                            pin(x[q & 1]);
+                            if (q < 3) tmem_ld32(t_s + 32 * (q + 1), x[(q + 1) & 1]);
+                            float a = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                a = max3(a, __uint_as_float(x[q & 1][i]), __uint_as_float(x[q & 1][i + 1]));
+                                b2 = max3(b2, __uint_as_float(x[q & 1][i + 2]), __uint_as_float(x[q & 1][i + 3]));
+                            }
+                            mt = max3(mt, a, b2);
+                        }
+                    }
+                    const float m_tile = mt * c2;
                     if (m_tile != m_tile) row_nan = true;
-                    const float m_new = fmaxf(m_run, m_tile);
                     bool resc = false;
                     float alpha = 1.f;
-                    if (m_new > m_run + 8.f) {
-                        alpha = ex2(m_run - m_new);         // 0 on the first tile with a visible key
+                    if (m_tile > m_run + 8.f) {
+                        alpha = ex2(m_run - m_tile);        // 0 on the first tile with a visible key
                         l2 = fma2(l2, f2(alpha, alpha), 0ull);
                         resc = jj >= step;                  // (O holds nothing before the group's second tile)
-                        m_run = m_new;
+                        m_run = m_tile;
                     }
                     const float mu = m_run == -INFINITY ? 0.f : m_run;
                     const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
-                    auto exps = [&](const uint32_t (&sc)[32], int col) {
-                        uint32_t pk[16];
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(t_s + 32 * q, x);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const uint64_t x2 = fma2(f2(__uint_as_float(sc[2 * k]), __uint_as_float(sc[2 * k + 1])), cc, nm);
+                            const uint64_t x2 = fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, nm);
                             float2 e;
-                            constexpr int kEvery = HTA_EXP2_POLY_EVERY;
-                            if (kEvery > 0 && k % kEvery == kEvery - 1) {
+                            if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
                                 e = exp2_poly2(x2);
                             } else {
-                                const float2 x = unf2(x2);
-                                e = make_float2(ex2(x.x), ex2(x.y));
+                                const float2 y = unf2(x2);
+                                e = make_float2(ex2(y.x), ex2(y.y));
                             }
                             pk[k] = pack_bf16x2(e.x, e.y);
                             l2 = add2(l2, f2(e.x, e.y));
                         }
-                        tmem_st16(t_s + col, pk);
-                    };
-                    if constexpr (!Q8) {
-                        exps(r0, 0);
-                        exps(r1, 16);
-                        exps(r2, 32);
-                        exps(r3, 48);
-                    } else {
-                        // P lands on columns 0..63, whose scores are in registers by then
-                        tmem_ld32(t_s + 0, r0);
-                        tmem_ld32(t_s + 32, r1);
-                        tmem_wait_ld();
-                        hide(r0, 0);
-                        hide(r1, 1);
-                        exps(r0, 0);
-                        exps(r1, 16);
-                        tmem_ld32(t_s + 64, r0);
-                        tmem_ld32(t_s + 96, r1);
-                        tmem_wait_ld();
-                        hide(r0, 2);
-                        hide(r1, 3);
-                        exps(r0, 32);
-                        exps(r1, 48);
+                        // P of these 32 keys on 16 columns whose scores have been read
+                        tmem_st16(t_s + 16 * q, pk);
                     }
                     if (__any_sync(0xffffffffu, resc)) {
                         // this tile's scores were committed after P*V of the group's previous
