@@ -51,7 +51,9 @@ namespace hta {
 
 namespace {
 
-constexpr int kPoisonRing = 8;
+// NaN words of the tiles in flight: K of tile p is there at the earliest when
+// the softmax of tile p - NK - 2 is done, so NK + 2 places are enough
+constexpr int kPoisonRing = 6;
 #ifndef HTA_POLY
 #define HTA_POLY 4
 #endif
@@ -70,8 +72,9 @@ struct Cfg {
     static constexpr int OFF_V = OFF_K + NK * TILE;
     static constexpr int OFF_BAR = OFF_V + NV * TILE;
     // q_full, q_empty, o_full, o_empty, drain, k_full[NK], k_empty[NK], k_raw[NK], v_full[NV], v_empty[NV],
-    // v_raw[NV], s_full[2], p_ready[2].  x_raw: a tile as TMA left it; x_full: ready for the MMAs
-    static constexpr int NUM_BARS = 5 + 3 * NK + 3 * NV + 4;
+    // v_raw[NV], s_full[2], p_ready[2][2] (halves of the keys).  x_raw: a tile as TMA left it; x_full: ready for the MMAs
+    static constexpr int NUM_BARS = 5 + 3 * NK + 3 * NV + 6;
+    static_assert(kPoisonRing >= NK + 2, "see kPoisonRing");
     static constexpr int OFF_POISON = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // [kPoisonRing][4] words
     static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort; Start
     static constexpr int OFF_PARENT = OFF_MISC + 64;                 // parent + 1 of each node, a byte (trees)
@@ -212,7 +215,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // (one arrive per loader warp, by TMA or by the fixer)
         for (int i = 0; i < C::NK; ++i) { mbar_init(k_full + i, Q8 ? 4 : 1); mbar_init(k_empty + i, 1); mbar_init(k_raw + i, 1); }
         for (int i = 0; i < C::NV; ++i) { mbar_init(v_full + i, Q8 ? 4 : 1); mbar_init(v_empty + i, 1); mbar_init(v_raw + i, 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(s_full + i, 1); mbar_init(p_ready + i, 4); }
+        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(p_ready + i, 4);
         mbar_init(drain, 1);
         *s_abort = 0;
         fence_barrier_init();
@@ -411,17 +415,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (!two || g == 0) {
                     ok = warp_wait(v_full + vst, vph);
                 }
-                if (ok) ok = warp_wait(p_ready + g, g ? cnt1 : cnt0);
+                const uint64_t vd = vdesc + ((vst * C::TILE) >> 4);
+                const bool done = !two || g == 1;
+                auto pv = [&](int kk) {
+                    mma_ts(tmem + C::COL_O + g * D, tmem + C::COL_S + g * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4), C::IDESC_PV,
+                           (s > 1 || kk > 0) ? 1u : 0u);
+                };
+                // the first 64 keys while the softmax group works on the others
+                if (ok) ok = warp_wait(p_ready + 2 * g, g ? cnt1 : cnt0);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) pv(kk);
+                }
+                ok = warp_wait(p_ready + 2 * g + 1, g ? cnt1 : cnt0);
                 if (!ok) break;
                 if (g) ++cnt1; else ++cnt0;
                 tc_fence_after();
-                const uint64_t vd = vdesc + ((vst * C::TILE) >> 4);
-                const bool done = !two || g == 1;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + C::COL_O + g * D, tmem + C::COL_S + g * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4),
-                               C::IDESC_PV, (s > 1 || kk > 0) ? 1u : 0u);
+                    for (int kk = 4; kk < 8; ++kk) pv(kk);
                     if (done) mma_commit(v_empty + vst);
                     if (s == n_steps - 1) mma_commit(o_full);
                 }
@@ -609,25 +623,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int row_hi = p.tree ? w.it.hi : (w.s.bad ? 0 : w.s.L + t + 1);
             const int row_lo = p.window > 0 ? max(0, row_hi - p.window) : 0;
 
+            const int it_base = w.it.base, it_all_lo = w.it.all_lo, it_all_hi = w.it.all_hi, it_cache_tiles = w.it.cache_tiles;
             float m_run = -INFINITY;
             uint64_t l2 = 0;
-            const int n_tiles = w.j1 - w.j0;
+            const int j0 = w.j0, n_tiles = w.j1 - j0;
             const int step = two ? 1 : 2;
             for (int jj = two ? 0 : grp; jj < n_tiles; jj += step) {
-                const int j = w.j0 + jj;
+                const int j = j0 + jj;
                 if (ok) ok = warp_wait(s_full + grp, cnt);
                 ++cnt;
                 tc_fence_after();
                 if (ok && warp_active) {
                     // the keys of a partly visible tile that this row sees
-                    const bool of_tree = j >= w.it.cache_tiles;
-                    const bool masked = of_tree || w.partial(j);
+                    const bool of_tree = j >= it_cache_tiles;
+                    const int key0 = it_base + j * 128;
+                    const bool masked = of_tree || key0 < it_all_lo || key0 + 128 > it_all_hi;
                     uint32_t see[4];
                     uint4 bad_v = make_uint4(0u, 0u, 0u, 0u);
                     if (Q8 && !of_tree) bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
                     if (masked) {
                         if (of_tree) {
-                            const int first = (j - w.it.cache_tiles) * 128;
+                            const int first = (j - it_cache_tiles) * 128;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see[i] = 0;
                             // (parents lie below their nodes, so the walk ends)
@@ -637,7 +653,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 for (int i = 0; i < 4; ++i) see[i] |= (d >> 5) == i ? 1u << (d & 31) : 0u;
                             }
                         } else {
-                            const int a = row_lo - w.key0(j), z = row_hi - w.key0(j);
+                            const int a = row_lo - key0, z = row_hi - key0;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see[i] = bit_range(a - 32 * i, z - 32 * i);
                         }
@@ -696,29 +712,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         resc = jj >= step;                  // (O holds nothing before the group's second tile)
                         m_run = m_tile;
                     }
-                    const float mu = m_run == -INFINITY ? 0.f : m_run;
-                    const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t x[32], pk[16];
-                        tmem_ld32(t_s + 32 * q, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const uint64_t x2 = fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, nm);
-                            float2 e;
-                            if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
-                                e = exp2_poly2(x2);
-                            } else {
-                                const float2 y = unf2(x2);
-                                e = make_float2(ex2(y.x), ex2(y.y));
-                            }
-                            pk[k] = pack_bf16x2(e.x, e.y);
-                            l2 = add2(l2, f2(e.x, e.y));
-                        }
-                        // P of these 32 keys on 16 columns whose scores have been read
-                        tmem_st16(t_s + 16 * q, pk);
-                    }
                     if (__any_sync(0xffffffffu, resc)) {
                         // this tile's scores were committed after P*V of the group's previous
                         // tile, so O[grp] is complete, and P*V of this tile waits for this warp
@@ -733,11 +726,50 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             tmem_st32(t_o + grp * D + col, ro);
                         }
                     }
-                    tmem_wait_st();
+                    const float mu = m_run == -INFINITY ? 0.f : m_run;
+                    const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(t_s + 32 * q, x);
+                        tmem_wait_ld();
+                        float2 e[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t x2 = fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, nm);
+                            if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
+                                e[k] = exp2_poly2(x2);
+                            } else {
+                                const float2 y = unf2(x2);
+                                e[k] = make_float2(ex2(y.x), ex2(y.y));
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(e[k].x, e[k].y);
+                        uint64_t la = f2(e[0].x, e[0].y), lb = f2(e[1].x, e[1].y);
+#pragma unroll
+                        for (int k = 2; k < 16; k += 2) {
+                            la = add2(la, f2(e[k].x, e[k].y));
+                            lb = add2(lb, f2(e[k + 1].x, e[k + 1].y));
+                        }
+                        l2 = add2(l2, add2(la, lb));
+                        // P of these 32 keys on 16 columns whose scores have been read
+                        tmem_st16(t_s + 16 * q, pk);
+                        if (q & 1) {
+                            tmem_wait_st();
+                            if (q == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(p_ready + 2 * grp);
+                            }
+                        }
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(p_ready + 2 * grp);     // (no rows in this warp, or the CTA gave up)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + grp);
+                if (lane == 0) mbar_arrive(p_ready + 2 * grp + 1);
             }
 
             // ------------------------------------------------------ epilogue
