@@ -170,27 +170,4 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Four e4m3 codes times 2^(e - 127), as two bf16 pairs, exactly: sign and
-// magnitude bits moved into bf16's fields (value * 2^-120, subnormal codes
-// landing on bf16 subnormals), then one product with mult = 2^(e - 7), given
-// twice as a bf16 pair (e = 255: NaN).
-__device__ __forceinline__ uint2 dequant_e4m3x4(uint32_t w, uint32_t mult) {
-    const uint32_t a = __byte_perm(w, 0, 0x1404);   // bytes 0, 1 in the upper halves of the two bf16
-    const uint32_t b = __byte_perm(w, 0, 0x3424);
-    const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-    const uint32_t y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-    uint2 r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(x), "r"(mult));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(y), "r"(mult));
-    return r;
-}
-
-// bf16 pair of 2^(e - 7) for a scale byte (a byte no append writes is
-// clamped into the range; 255 gives NaN).
-__device__ __forceinline__ uint32_t e4m3_mult(int e) {
-    const uint32_t h = e == kScaleNan ? 0x7fc0u
-                                      : static_cast<uint32_t>(min(max(e, kScaleMin), kScaleMax) + 120) << 7;
-    return h | (h << 16);
-}
-
 }  // namespace hta

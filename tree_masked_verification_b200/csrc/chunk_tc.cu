@@ -23,21 +23,29 @@
 // Warps: 0 TMA producer of K, 1 MMA issuer, 2 TMA producer of V, 3 fixer of
 // partly visible V tiles (bf16 caches), 4-7 and 8-11 two softmax groups (one
 // row per thread), 12-19 loaders (e4m3 caches).  TMA leaves a tile's codes in
-// the upper half of its stage; the loaders read them into registers and
-// write the whole stage over as the swizzled bf16 tile the MMAs read (an
-// exact product, see dequant_e4m3x4), so that codes need no buffers of their
-// own and the rings prefetch as deep as for bf16.  (Loads straight into
-// registers, one tile ahead, took 5 us a tile: a warp's waits on them cover
-// younger loads too, so that each tile waited for the next one's.)  With two
+// the upper half of its stage; the loaders read them into registers and write
+// the whole stage over as the swizzled f16 tile the MMAs read, so that codes
+// need no buffers of their own and the rings prefetch as deep as for bf16.
+// (Loads straight into registers, one tile ahead, took 5 us a tile: a warp's
+// waits on them cover younger loads too, so that each tile waited for the
+// next one's.)  e4m3 caches run the MMAs in f16: a code is one of f16's
+// numbers, two to a conversion, where bf16 took ten integer operations for
+// four and the integer pipe was the bound.  A tile's rows are scaled to its
+// largest scale E (rows 2^-24 below it vanish beside it), 2^(E - 127) goes to
+// the scores, or for V to the weights: against a running reference E_run, by
+// which the output is multiplied at the end.  E is at least 96 (V of 1e-7: an
+// all-zero tile must not drive the weights out of fp32's range).  Query rows
+// are scaled by powers of two into f16, which holds bf16's 8 bits down to
+// 2^-28 of the row's largest value.  With two
 // row tiles group g owns tile g and runs every key tile; with one, group g runs the key tiles j = g mod 2 into
 // an accumulator of its own and the two are merged at the end (the lse merge
 // of two key ranges).  Steps s of an item: group s & 1, key tile
 // s >> (two row tiles); MMA order QK_0 QK_1 [PV_0 QK_2] [PV_1 QK_3] ...
 //
-// Tensor memory: S[g] columns 128g.. (fp32 scores; P as bf16 pairs over its
-// first 64), O[g] columns 256 + gD...  P is rounded to bf16 for the tensor
-// cores (relative 2^-9 on average, the same size as the output's own
-// rounding); its sum l, the maximum and O stay in fp32.  The running maximum
+// Tensor memory: S[g] columns 128g.. (fp32 scores; P as 16-bit pairs over its
+// first 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
+// for the tensor cores, relative 2^-9 on average, the same size as the output's
+// own rounding; its sum l, the maximum and O stay in fp32.  The running maximum
 // moves only when it grew by more than 2^8 (exact after the division by l).
 //
 // Keys a row does not see: scores are set to -inf, and rows of V that no row
@@ -61,8 +69,11 @@ constexpr int kPolyEvery = HTA_POLY;               // one exp2 pair in this many
 
 template <int D, bool Q8>
 struct Cfg {
-    static constexpr int NK = D == 128 ? 3 : 4;             // K ring depth
-    static constexpr int NV = D == 128 ? 2 : 4;             // V ring depth
+#ifndef HTA_NK
+#define HTA_NK 3
+#endif
+    static constexpr int NK = D == 128 ? HTA_NK : 4;             // K ring depth
+    static constexpr int NV = D == 128 ? 5 - HTA_NK : 4;             // V ring depth
     static constexpr int HALVES = D / 64;                   // 64-column swizzle boxes
     static constexpr int BOX = 128 * 64 * 2;
     static constexpr int TILE = 128 * D * 2;
@@ -81,21 +92,23 @@ struct Cfg {
     static constexpr int OFF_SCALE = OFF_PARENT + kTMax;             // per K stage: scale bytes of K and of V; per V stage: V's
     static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 + NV * 128 : 0);   // walks: softmax groups, K and V loaders
     static constexpr int WALK_BYTES = 128;
-    static constexpr int SMEM = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;
-    static constexpr int SMEM_ALLOC = SMEM + 1024;          // slack to align the base to 1024
-    static constexpr int OFF_XCH = TILE;                    // [2][2][128] floats, in the unused second Q tile
+    static constexpr int OFF_EXP = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;   // per tile in flight: E of K, E of V
+    static constexpr int OFF_RED = OFF_EXP + (Q8 ? kPoisonRing * 8 : 0);   // [2][4] words: a maximum over a loader set
+    static constexpr int SMEM_ALLOC = OFF_RED + (Q8 ? 32 : 0);
+    static constexpr int OFF_XCH = TILE;                    // [2][3][128] floats, in the unused second Q tile
     static constexpr int OFF_PLAN = OFF_K;                  // int64 [kPlanUnits], before the first copy
     static constexpr int THREADS = Q8 ? 640 : 384;
     // registers per thread; the launch allots LAUNCH_REGS to each
     static constexpr int LAUNCH_REGS = Q8 ? 96 : 168;
-    static constexpr int REGS_SOFTMAX = Q8 ? 152 : 224;
-    static constexpr int REGS_LOAD = 56;
+    static constexpr int REGS_SOFTMAX = Q8 ? 136 : 224;
+    static constexpr int REGS_LOAD = 72;
     static constexpr int REGS_OTHER = Q8 ? 64 : 56;
     static_assert(256 * REGS_SOFTMAX + (Q8 ? 256 * REGS_LOAD : 0) + 128 * REGS_OTHER <= THREADS * LAUNCH_REGS,
                   "register split must fit the launch allocation");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
-    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false);
-    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
+    static constexpr uint32_t F16 = Q8 ? ~((1u << 7) | (1u << 10)) : ~0u;   // (format 1 of A and B: bf16, 0: f16)
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false) & F16;
+    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true) & F16;
     static constexpr int COL_S = 0, COL_O = 256;
 };
 
@@ -144,6 +157,47 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+// 2^d in f16 (d <= 0; 0 below 2^-24), twice
+__device__ __forceinline__ uint32_t f16_pow2(int d) {
+    const uint32_t h = d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+    return h | (h << 16);
+}
+// four e4m3 codes times an f16 pair `mult`, as two f16 pairs
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w, uint32_t mult) {
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 a, b;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 a, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 b, hi;\n\t"
+        "mul.rn.f16x2 %0, a, %3;\n\t"
+        "mul.rn.f16x2 %1, b, %3;\n\t}"
+        : "=r"(r.x), "=r"(r.y) : "r"(w), "r"(mult));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float pow2(int d) { return __uint_as_float(static_cast<uint32_t>(127 + d) << 23); }
+// largest |bf16| bit pattern of eight values and `big`
+__device__ __forceinline__ uint32_t max_bits(uint4 u, uint32_t big) {
+    big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
+    return __vmaxu2(big, u.w & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint32_t halves_max(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+// eight bf16 values times `mul`, as f16
+__device__ __forceinline__ uint4 to_f16(uint4 u, float mul) {
+    return make_uint4(pack_f16x2(bf16_lo(u.x) * mul, bf16_hi(u.x) * mul), pack_f16x2(bf16_lo(u.y) * mul, bf16_hi(u.y) * mul),
+                      pack_f16x2(bf16_lo(u.z) * mul, bf16_hi(u.z) * mul), pack_f16x2(bf16_lo(u.w) * mul, bf16_hi(u.w) * mul));
+}
+// the shift that brings a largest bit pattern into [2^14, 2^15), within [-100, most]
+__device__ __forceinline__ int f16_shift(uint32_t big, int most) {
+    return max(min(14 - (static_cast<int>(big >> 7) - 127), most), -100);
+}
+
+constexpr int kLeastE = 96;         // least scale of a tile
+
 // registers of a tensor-memory load that has been waited for
 __device__ __forceinline__ void pin(uint32_t (&r)[32]) {
 #pragma unroll
@@ -191,9 +245,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                 const __grid_constant__ ChunkParams p) {
     using C = Cfg<D, Q8>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {                   // (the swizzled tiles need it; every slot is left empty)
+        if (threadIdx.x == 0) {
+            raise_status(p.status, kStatusInternal);
+            p.heads[2 * blockIdx.x].rows = p.heads[2 * blockIdx.x + 1].rows = 0;
+        }
+        return;
+    }
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 1, *o_full = bars + 2, *o_empty = bars + 3, *drain = bars + 4;
@@ -206,6 +266,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     Start *s_start = reinterpret_cast<Start *>(smem + C::OFF_MISC + 16);
     uint8_t *s_parent = smem + C::OFF_PARENT;       // (parent + 1)
     uint8_t *s_scale = smem + C::OFF_SCALE;
+    int2 *s_exp = reinterpret_cast<int2 *>(smem + C::OFF_EXP);
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 8);                       // one arrive per softmax warp
@@ -450,14 +511,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // ------------- loaders (e4m3 cache): four warps for K, four for V
         if constexpr (Q8) {
             regs_dec<C::REGS_LOAD>();
-            constexpr int LPR = D / 8;              // lanes per cache row (8 codes each)
-            constexpr int RW = 32 / LPR;            // rows of a warp and round
-            constexpr int BATCH = D == 128 ? 4 : 8;  // rounds of loads in flight (D = 64: all, see convert)
             const bool is_v = warp >= kWarpLoad + 4;
-            const int lw = (warp - kWarpLoad) & 3, c = lane % LPR, set_bar = is_v ? 3 : 2;
-            // a warp has the rows lw * 32 ..; its lane's place in the swizzle
-            // alternates with the round where a round is not a multiple of 8 rows
-            const int row0 = lw * 32 + lane / LPR;
+            const int lw = (warp - kWarpLoad) & 3, set_bar = is_v ? 3 : 2;
+            // A lane converts one row, 8 codes at a time, in an order of its own: piece
+            // i ^ turn.  The turns are chosen such that 16 lanes' loads meet 16 different
+            // 8-byte banks and 8 lanes' stores 8 different 16-byte ones behind the
+            // swizzle (D = 128: r -> 2r in GF(8), for which r and r + 2r are both
+            // permutations; D = 64, two rows to 128 bytes: r >> 1).
+            const int row = lw * 32 + lane;
+            const uint32_t turn = D == 128 ? (((lane << 1) & 6) ^ (lane & 4 ? 3 : 0)) | (lane & 8) : (lane >> 1) & 7;
+            const uint32_t raw_off = C::TILE - C::RAW + row * D, out_off = row * 128;
             Walk &lwk = *reinterpret_cast<Walk *>(smem + C::OFF_WALK + (is_v ? 2 : 1) * C::WALK_BYTES);
             volatile int *more = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(&lwk) + C::WALK_BYTES - 4);
             const bool first_thread = lw == 0 && lane == 0;
@@ -467,30 +530,38 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             int st = 0, ph = 0, pos = 0;
             bool ok = true;
             if (first_thread) lwk.start(p, s_start);
-            // A stage's codes to bf16, in place; lane l holds the multiplier of row
-            // lw * 32 + l, 0 for rows that are no keys.  At D = 128 a row's codes lie
-            // where its own second half goes, so a warp needs no other's progress;
-            // at D = 64 they lie where other warps' rows go.
-            auto convert = [&](uint8_t *stage, uint32_t mult) {
-                const uint8_t *src = stage + C::TILE - C::RAW + c * 8;
-                auto part = [&](int i0, bool sync) {
-                    uint2 u[BATCH];
+            // A stage's codes to f16, in place, times the row's `mult` (0: zeros).  At
+            // D = 128 a row's codes lie where its own second half goes, so a lane needs
+            // no other's progress; at D = 64 they lie where other warps' rows go.  All
+            // loads of the row first: beside the tensor-memory traffic a load from shared
+            // memory takes hundreds of cycles (four at a time, with the multipliers by
+            // shuffles: 2400 cycles a tile).
+            uint2 u[D / 8];
+            auto read_row = [&](const uint8_t *stage) {
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) u[i] = *reinterpret_cast<const uint2 *>(src + (row0 + (i0 + i) * RW) * D);
-                    if (sync) bar_sync(set_bar, 128);
-                    else __syncwarp();
+                for (int i = 0; i < D / 8; ++i) u[i] = *reinterpret_cast<const uint2 *>(stage + raw_off + ((turn ^ i) << 3));
+            };
+            auto write_row = [&](uint8_t *stage, uint32_t mult) {
+                if (D == 64) bar_sync(set_bar, 128);
+                const uint32_t keep = mult ? 0xffffffffu : 0u;      // (NaN codes)
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = row0 + (i0 + i) * RW;
-                        const uint32_t m = __shfl_sync(0xffffffffu, mult, (i0 + i) * RW + lane / LPR);
-                        const uint2 a = dequant_e4m3x4(u[i].x, m), b = dequant_e4m3x4(u[i].y, m);
-                        *reinterpret_cast<uint4 *>(stage + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(a.x, a.y, b.x, b.y);
-                    }
-                };
-                static_assert(D == 128 || 32 / RW == BATCH, "one batch where rows overlap other warps'");
-#pragma unroll 1
-                for (int i = 0; i < 32 / RW; i += BATCH) part(i, D != 128);
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint2 a = e4m3x4_to_f16x4(u[i].x & keep, mult), b = e4m3x4_to_f16x4(u[i].y & keep, mult);
+                    const uint32_t c = turn ^ i;
+                    *reinterpret_cast<uint4 *>(stage + (c >> 3) * C::BOX + out_off + (((c & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(a.x, a.y, b.x, b.y);
+                }
+            };
+            // largest scale byte of the live rows [a, z) (NaN rows aside), at least
+            // kLeastE; w4: bytes of rows 4 * lane ..
+            auto tile_exp = [&](uint32_t w4, int a, int z) {
+                int e = kLeastE;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = (w4 >> (8 * i)) & 255, r = 4 * lane + i;
+                    if (r >= a && r < z && x != kScaleNan) e = max(e, x);
+                }
+                return min(static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(e))), kScaleMax);
             };
             for (;;) {
                 bar_sync(set_bar, 128);
@@ -502,37 +573,51 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 for (int j = j0; j < j1; ++j, ++pos) {
                     uint8_t *stage = ring + st * C::TILE;
                     if (ok) ok = warp_wait(raw + st, ph);
-                    uint32_t *word = s_poison + (pos % kPoisonRing) * 4 + lw;
+                    const int at = pos % kPoisonRing;
+                    uint32_t *word = s_poison + at * 4 + lw;
                     if (j < cache_tiles) {
-                        const int r = lw * 32 + lane, key = base + j * 128 + r;
-                        const bool live = key >= lo && key < hi;
+                        const int a = lo - (base + j * 128), z = hi - (base + j * 128);
+                        const bool live = row >= a && row < z;
                         const uint8_t *sc = is_v ? s_scale + C::NK * 256 + st * 128 : s_scale + st * 256;
-                        const int e = sc[r];
+                        const uint8_t *scv = is_v ? sc : sc + 128;
+                        read_row(stage);
+                        const int e = sc[row], ev = scv[row];
+                        const uint32_t e4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
+                        const uint32_t ev4 = *reinterpret_cast<const uint32_t *>(scv + 4 * lane);
+                        const int E = tile_exp(e4, a, z);
                         if (!is_v) {
-                            // V rows held as NaN are told to the softmax groups with K, before they read the scores
-                            const uint32_t nan = __ballot_sync(0xffffffffu, live && sc[128 + r] == kScaleNan);
+                            // V rows held as NaN, and V's E, are told to the softmax groups with K
+                            const uint32_t nan = __ballot_sync(0xffffffffu, live && ev == kScaleNan);
+                            const int Ev = tile_exp(ev4, a, z);
                             if (lane == 0) *word = nan;
+                            if (first_thread) s_exp[at] = make_int2(E, Ev);
                         }
-                        convert(stage, live && !(is_v && e == kScaleNan) ? e4m3_mult(e) : 0u);
-                    } else if (is_v) {
-                        // tree rows, one a lane: rows behind the tree are zeroed, and so are rows
-                        // with an infinity or a NaN, which are told to the softmax groups (they
-                        // wait for this tile).  K rows behind the tree are masked.
+                        write_row(stage, !live ? 0u : e != kScaleNan ? f16_pow2(min(e - E, 0)) : is_v ? 0u : 0x7e007e00u);
+                    } else {
+                        // tree rows (bf16), one a lane, scaled into f16 by the tile's largest value.
+                        // Rows behind the tree are zeroed, and so are V rows with an infinity or a
+                        // NaN, which are told to the softmax groups (they wait for this tile).
                         const int r = lw * 32 + lane, live = min(128, p.N - (j - cache_tiles) * 128);
                         uint8_t *rp = stage + r * 128;
+                        auto piece = [&](int x) { return reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)); };
                         uint32_t big = 0;
 #pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4));
-                            big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
-                            big = __vmaxu2(big, u.w & 0x7fff7fffu);
+                        for (int x = 0; x < D / 8; ++x) big = max_bits(*piece(x), big);
+                        big = halves_max(big);
+                        const bool inf = big >= 0x7f80u, zero = r >= live || (is_v && inf);
+                        uint32_t *red = reinterpret_cast<uint32_t *>(smem + C::OFF_RED) + (is_v ? 4 : 0);
+                        const uint32_t wm = __reduce_max_sync(0xffffffffu, r < live && !inf ? big : 0u);
+                        bar_sync(set_bar, 128);
+                        if (lane == 0) red[lw] = wm;
+                        bar_sync(set_bar, 128);
+                        const int up = f16_shift(max(max(red[0], red[1]), max(red[2], red[3])), 127 - kLeastE);
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) *piece(x) = zero ? make_uint4(0u, 0u, 0u, 0u) : to_f16(*piece(x), pow2(up));
+                        if (is_v) {
+                            const uint32_t nan = __ballot_sync(0xffffffffu, r < live && inf);
+                            if (lane == 0) *word = nan;
                         }
-                        const bool inf = r < live && max(big & 0xffffu, big >> 16) >= 0x7f80u;
-                        if (r >= live || inf)
-                            for (int x = 0; x < D / 8; ++x)
-                                *reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t nan = __ballot_sync(0xffffffffu, inf);
-                        if (lane == 0) *word = nan;
+                        if (first_thread) (is_v ? s_exp[at].y : s_exp[at].x) = 127 - up;
                     }
                     fence_proxy_async();
                     __syncwarp();
@@ -550,7 +635,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t t_s = tmem + lane_addr + C::COL_S + grp * 128;
         const uint32_t t_o = tmem + lane_addr + C::COL_O;
-        const float c2 = p.scale_log2, nan = __int_as_float(0x7fc00000);
+        const float nan = __int_as_float(0x7fc00000);
         int cnt = 0, items = 0, pos = 0;                    // steps of this group, items, key tiles so far
         bool ok = true;
         // One walk for both groups, in shared memory: its thirty values would
@@ -587,21 +672,33 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             if (w.s.bad && first_thread) raise_status(p.status, kStatusPrefixLenRange);
             bool row_nan = w.s.bad;
+            float c2_row = p.scale_log2;
             // ---- Q into shared memory (one row tile: each group half of the columns)
             {
                 const int ch0 = two ? 0 : grp * (D / 16), nch = two ? D / 8 : D / 16;
                 uint4 qv[D / 8];
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
-                    if (i < nch) qv[i] = valid ? reinterpret_cast<const uint4 *>(qp)[ch0 + i] : make_uint4(0u, 0u, 0u, 0u);
+                    if (Q8 || i < nch)
+                        qv[i] = valid ? reinterpret_cast<const uint4 *>(qp)[Q8 ? i : ch0 + i] : make_uint4(0u, 0u, 0u, 0u);
+                float mul = 1.f;
+                if constexpr (Q8) {                     // (the shift takes the whole row's largest value)
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) big = max_bits(qv[i], big);
+                    const int up = f16_shift(halves_max(big), 100);
+                    mul = pow2(up);
+                    c2_row = p.scale_log2 * pow2(-up);
+                }
                 if (ok) ok = warp_wait(q_empty, items + 1);
                 uint8_t *qs = smem + C::OFF_Q + (two ? grp * C::TILE : 0) + r * 128;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    if (i < nch) {
-                        const int ch = ch0 + i;
-                        *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::BOX + (((ch & 7) ^ (r & 7)) << 4)) = qv[i];
-                    }
+                for (int i = 0; i < D / 8; ++i) {
+                    const int ch = Q8 ? i : ch0 + i;
+                    if (Q8 ? i >= ch0 && i < ch0 + nch : i < nch)
+                        *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::BOX + (((ch & 7) ^ (r & 7)) << 4)) =
+                            Q8 ? to_f16(qv[i], mul) : qv[i];
+                }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
@@ -625,6 +722,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
             const int it_base = w.it.base, it_all_lo = w.it.all_lo, it_all_hi = w.it.all_hi, it_cache_tiles = w.it.cache_tiles;
             float m_run = -INFINITY;
+            int e_run = 0;                                  // (e4m3) scale of O: 2^(e_run - 127)
             uint64_t l2 = 0;
             const int j0 = w.j0, n_tiles = w.j1 - j0;
             const int step = two ? 1 : 2;
@@ -667,6 +765,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     } else if (Q8) {
                         if (bad_v.x | bad_v.y | bad_v.z | bad_v.w) row_nan = true;
                     }
+                    float c2 = c2_row;
+                    bool resc = false;
+                    float alpha = 1.f, shift = 0.f;         // P is 2^(x - m + shift)
+                    if constexpr (Q8) {
+                        const int2 E = s_exp[(pos + jj) % kPoisonRing];
+                        c2 *= pow2(E.x - 127);
+                        // f16 holds 2^8 (the stale maximum) times 2^7: only a larger step moves e_run
+                        if (jj < step) {
+                            e_run = E.y;
+                        } else if (E.y > e_run + 7) {
+                            alpha = ex2(static_cast<float>(e_run - E.y));
+                            resc = true;
+                            e_run = E.y;
+                        }
+                        shift = static_cast<float>(E.y - e_run);
+                    }
                     // Three short loops over the row's 128 scores, 32 at a time, from
                     // tensor memory each time: the code stays small.  (Unrolled over all
                     // 128 it was fetched, not issued, at the pace the five roles that
@@ -704,11 +818,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     const float m_tile = mt * c2;
                     if (m_tile != m_tile) row_nan = true;
-                    bool resc = false;
-                    float alpha = 1.f;
                     if (m_tile > m_run + 8.f) {
-                        alpha = ex2(m_run - m_tile);        // 0 on the first tile with a visible key
-                        l2 = fma2(l2, f2(alpha, alpha), 0ull);
+                        const float a = ex2(m_run - m_tile);   // 0 on the first tile with a visible key
+                        l2 = fma2(l2, f2(a, a), 0ull);
+                        alpha *= a;
                         resc = jj >= step;                  // (O holds nothing before the group's second tile)
                         m_run = m_tile;
                     }
@@ -726,8 +839,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             tmem_st32(t_o + grp * D + col, ro);
                         }
                     }
-                    const float mu = m_run == -INFINITY ? 0.f : m_run;
+                    const float mu = (m_run == -INFINITY ? 0.f : m_run) - shift;
                     const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
+                    uint64_t lt = 0;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t x[32], pk[16];
@@ -745,14 +859,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(e[k].x, e[k].y);
+                        for (int k = 0; k < 16; ++k) pk[k] = Q8 ? pack_f16x2(e[k].x, e[k].y) : pack_bf16x2(e[k].x, e[k].y);
                         uint64_t la = f2(e[0].x, e[0].y), lb = f2(e[1].x, e[1].y);
 #pragma unroll
                         for (int k = 2; k < 16; k += 2) {
                             la = add2(la, f2(e[k].x, e[k].y));
                             lb = add2(lb, f2(e[k + 1].x, e[k + 1].y));
                         }
-                        l2 = add2(l2, add2(la, lb));
+                        lt = add2(lt, add2(la, lb));
                         // P of these 32 keys on 16 columns whose scores have been read
                         tmem_st16(t_s + 16 * q, pk);
                         if (q & 1) {
@@ -763,6 +877,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 if (lane == 0) mbar_arrive(p_ready + 2 * grp);
                             }
                         }
+                    }
+                    if constexpr (Q8) {
+                        const float back = ex2(-shift);
+                        l2 = fma2(lt, f2(back, back), l2);
+                    } else {
+                        l2 = add2(l2, lt);
                     }
                 } else if (lane == 0) {
                     mbar_arrive(p_ready + 2 * grp);     // (no rows in this warp, or the CTA gave up)
@@ -778,20 +898,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float2 lp = unf2(l2);
             float l = m_run == -INFINITY ? 0.f : lp.x + lp.y, m = m_run;
             float a0 = 1.f, a1 = 0.f;
+            float o0 = Q8 ? pow2(e_run - 127) : 1.f, o1 = 1.f;      // scales of O[0], O[1] (two row tiles: of the own)
             bool has1 = false;
             if (!two) {                                     // join the groups: key tiles 0, 2, .. and 1, 3, ..
                 float *xch = reinterpret_cast<float *>(smem + C::OFF_XCH);
-                xch[(grp * 2 + 0) * 128 + r] = m;
-                xch[(grp * 2 + 1) * 128 + r] = l;
-                row_nan = row_nan | (ok ? false : true);
-                // (row_nan of either group: through the sum)
-                if (row_nan) xch[(grp * 2 + 1) * 128 + r] = nan;
+                xch[(grp * 3 + 0) * 128 + r] = m;
+                xch[(grp * 3 + 1) * 128 + r] = row_nan || !ok ? nan : l;   // (a bad row of either group: through the sum)
+                xch[(grp * 3 + 2) * 128 + r] = o0;
                 bar_sync(1, 256);
-                const float m0 = xch[r], m1 = xch[2 * 128 + r];
+                const float m0 = xch[r], m1 = xch[3 * 128 + r];
                 m = fmaxf(m0, m1);
                 a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
                 a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
-                const float l0 = xch[128 + r], l1 = xch[3 * 128 + r];
+                const float l0 = xch[128 + r], l1 = xch[4 * 128 + r];
+                o0 = xch[2 * 128 + r];
+                o1 = xch[5 * 128 + r];
                 l = a0 * l0 + a1 * l1;
                 row_nan = l0 != l0 || l1 != l1;
                 has1 = n_tiles > 1;
@@ -806,7 +927,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const long long prow = slot_row(p, blockIdx.x, which) + row;
             const int col0 = two ? 0 : grp * (D / 2), col1 = two ? D : col0 + D / 2;
             if (warp_active) {
-                const float f0 = a0 * inv, f1 = a1 * inv;
+                const float f0 = a0 * inv * o0, f1 = a1 * inv * o1;
                 const uint32_t to0 = t_o + (two ? grp * D : 0), to1 = t_o + D;
 #pragma unroll 1
                 for (int col = col0; col < col1; col += 32) {
