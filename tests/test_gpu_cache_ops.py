@@ -474,3 +474,171 @@ def test_prompt_decode_verify_commit_run(q8):
     spread = float(held.abs().max())
     tol = (4 * P.BF16 + 6e-3 if not q8 else 0.1) * spread
     assert (again[0].float() - out[0, :, 3].float()).abs().max() <= tol
+
+
+# ------------------------------------------------- what only bad values reach
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("Hq,new", [(8, 200), (4, 40), (2, 3)])
+def test_masked_rows_may_hold_anything(q8, Hq, new):
+    """An infinity or a NaN in the K or V of a token reaches the rows that see
+    it (as NaN) and no other: not the earlier tokens of its chunk, not those
+    whose window has passed it."""
+    D, bs, pre, window = 128, 16, 150, 64
+    c = Case([pre], [new], Hq, 2, D, bs, q8, seed=12)
+    good = {w: c.attend(w)[0] for w in (0, window)}
+    bad_at = pre + new // 2
+    blk, at = int(c.table[0, bad_at // bs]), bad_at % bs
+    for cache, scale, value in ((c.kc, c.ks, math.nan), (c.vc, c.vs, math.inf)):
+        keep = (cache.clone(), None if scale is None else scale.clone())
+        if q8:
+            cache.view(torch.uint8)[blk, :, at] = 0x7f
+            scale[blk, :, at] = 255
+        else:
+            cache[blk, :, at, 5] = value
+        for w in (0, window):
+            out, lse, code = c.attend(w)
+            assert code == hta.OK
+            sees = [pre + t >= bad_at and (w == 0 or pre + t - w < bad_at) for t in range(new)]
+            for t in range(new):
+                if sees[t]:
+                    assert not torch.isfinite(out[t].float()).all(-1).any(), (t, w)
+                else:
+                    assert torch.equal(out[t], good[w][t]), (t, w)
+        cache.copy_(keep[0])
+        if q8:
+            scale.copy_(keep[1])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_blocks_before_the_window_need_no_entry(q8):
+    c = Case([500, 3], [20, 20], 8, 2, 128, 16, q8, seed=5)
+    good, _, _ = c.attend(100)
+    c.table[0, :(500 - 99) // 16] = -1                # wholly before every token's window
+    out, _, code = c.attend(100)
+    assert code == hta.OK and torch.equal(out, good)
+
+
+def test_verify_q8_bad_tree_rows_reach_their_descendants_only():
+    c = Case([200], [0], 4, 2, 128, 16, True, seed=1)
+    T = 130
+    q, kt, vt = randn(1, 4, T, 128, seed=1), randn(1, 2, T, 128, seed=2), randn(1, 2, T, 128, seed=3)
+    parent = torch.tensor([[-1 if i < 4 else i - 4 for i in range(T)]], dtype=torch.int32).cuda()
+    good, _ = hta.verify_paged(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, **c.paged())
+    for t, value in ((kt, math.nan), (vt, math.inf), (vt, math.nan)):
+        keep = t.clone()
+        t[0, :, 9, 3] = value
+        out, _ = hta.verify_paged(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, **c.paged())
+        t.copy_(keep)
+        for i in range(T):
+            if i >= 9 and i % 4 == 1:
+                assert not torch.isfinite(out[0, :, i].float()).all(-1).any(), i
+            else:
+                assert torch.equal(out[0, :, i], good[0, :, i]), i
+
+
+# --------------------------------------------------------- sizes and schedules
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("pre,new,Hq,Hkv,D,bs", [
+    ([700, 3, 40], [1, 1, 1], 16, 1, 128, 16), ([700, 3, 40], [1, 1, 1], 16, 1, 64, 32),
+    ([100, 5, 1], [3, 1, 0], 8, 2, 64, 16), ([2000, 9], [1, 1], 3, 1, 128, 128), ([5] * 70, [1] * 70, 6, 2, 64, 16)])
+def test_chunk_attention_few_rows(pre, new, Hq, Hkv, D, bs, q8):
+    Case(pre, new, Hq, Hkv, D, bs, q8, seed=len(pre)).check()
+    Case(pre, new, Hq, Hkv, D, bs, q8, seed=len(pre)).check(window=33)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_thousands_of_sequences(q8):
+    """More sequences than the schedule keeps one by one."""
+    g = torch.Generator().manual_seed(1)
+    pre = torch.randint(0, 20, (2300,), generator=g).tolist()
+    new = torch.randint(0, 3, (2300,), generator=g).tolist()
+    c = Case(pre, new, 2, 1, 64, 16, q8, seed=3)
+    rows = {(t, h) for t in range(0, c.N, 97) for h in (0, 1)}
+    c.check(rows=rows)
+    out, _, _ = c.attend()
+    assert torch.isfinite(out.float()).all()
+
+
+def test_no_tokens_at_all():
+    c = Case([7, 3], [0, 0], 4, 2, 64, 16, seed=1)
+    out, lse, code = c.attend()
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and code == hta.OK
+    before = c.kc.clone()
+    hta.append_paged(randn(0, 2, 64), randn(0, 2, 64), c.kc, c.vc, c.table, c.prefix_len, c.q_start, **c.paged())
+    assert torch.equal(before.view(torch.uint8), c.kc.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_a_captured_call_follows_the_lengths(q8):
+    """Two graphs over one workspace, replayed after the lengths and the chunks
+    on the device have changed, on another stream than the capture's."""
+    c = Case([300, 40, 0], [30, 1, 70], 8, 2, 128, 32, q8, seed=8)
+    ws = hta.new_chunk_workspace(c.q, c.kc, 3, L_cap=c.L_cap)
+    out, lse = torch.zeros_like(c.q), torch.zeros(c.q.shape[:2], device="cuda")
+
+    def call(window):
+        hta.chunk_attention_paged(c.q, c.kc, c.vc, c.table, c.prefix_len, c.q_start, window=window, workspace=ws,
+                                  out=out, lse=lse, **c.paged())
+    call(0)
+    torch.cuda.synchronize()
+    graphs = []
+    for window in (0, 50):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(window)
+        graphs.append((g, window))
+    side = torch.cuda.Stream()
+    for pre, start in (([300, 40, 0], [0, 30, 31, 101]), ([290, 0, 7], [0, 2, 2, 40]), ([0, 40, 69], [0, 100, 100, 101])):
+        c.prefix_len.copy_(torch.tensor(pre, dtype=torch.int32))
+        c.q_start.copy_(torch.tensor(start, dtype=torch.int32))
+        for g, window in graphs:
+            want, want_lse, code = c.attend(window)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                g.replay()
+            torch.cuda.current_stream().wait_stream(side)
+            n = start[-1]
+            assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_lse[:n])
+
+
+def test_equal_calls_give_equal_bits():
+    """Nothing depends on the order in which CTAs finish."""
+    for q8 in (False, True):
+        c = Case([4000, 100, 9], [5, 300, 1], 8, 2, 128, 64, q8, seed=2)
+        first = c.attend()[:2]
+        for _ in range(5):
+            again = c.attend()[:2]
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+def test_wide_range_of_scales():
+    """Rows of 1e-6 and of 1e3 in one e4m3 cache, K and V: each row's weight is
+    right, whatever the others' scales."""
+    for new, Hq in (([40], 4), ([1], 4), ([300], 2)):
+        c = Case([260], new, Hq, 2, 128, 16, True, seed=3)
+        for cache, scale in ((c.kc, c.ks), (c.vc, c.vs)):
+            e = scale.int()
+            live = e != 255
+            g = torch.Generator(device="cuda").manual_seed(1)
+            step = torch.randint(-20, 11 if scale is c.vs else 1, e.shape, generator=g, device="cuda")
+            scale.copy_(torch.where(live, (e + step).clamp(16, 134), e).to(torch.uint8))
+        c.check()
+
+
+def test_workspaces_and_devices_are_checked():
+    c = Case([40, 20], [4, 3], 4, 2, 64, 16, seed=3)
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(hta.HtaError) as e:
+        hta.chunk_attention_paged(c.q, c.kc, c.vc, c.table, c.prefix_len, c.q_start, workspace=small, **c.paged())
+    assert e.value.code == hta.ERR_WORKSPACE_TOO_SMALL
+    with pytest.raises(hta.HtaError) as e:
+        hta.append_paged(randn(7, 2, 64), randn(7, 2, 64), c.kc, c.vc, c.table, c.prefix_len, c.q_start,
+                         workspace=small[:128], **c.paged())
+    assert e.value.code == hta.ERR_WORKSPACE_TOO_SMALL
+    with pytest.raises(ValueError):
+        hta.append_paged(randn(7, 2, 64).cpu(), randn(7, 2, 64), c.kc, c.vc, c.table, c.prefix_len, c.q_start, **c.paged())
+    with pytest.raises(ValueError):
+        hta.chunk_attention_paged(c.q, c.kc, c.vc, c.table, c.prefix_len.cpu(), c.q_start, **c.paged())
+    with pytest.raises(hta.HtaError) as e:
+        hta.chunk_attention_paged(c.q, c.kc, c.vc, c.table, c.prefix_len, c.q_start, window=-1, **c.paged())
+    assert e.value.code == hta.ERR_INVALID_OPTION

@@ -168,7 +168,8 @@ int longspec_hta_qk_norm_rope(int B, int T, int Hq, int Hkv, int D, const longsp
                               const longspec_hta_heads *k, const int32_t *positions, const longspec_hta_rope *rope,
                               const longspec_hta_heads *q_out, const longspec_hta_heads *k_out,
                               cudaStream_t stream) {
-    if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || 1LL * B * T * (Hq > Hkv ? Hq : Hkv) >= kIntLimit)
+    if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || 1LL * B * T >= kIntLimit ||
+        1LL * B * T * (Hq > Hkv ? Hq : Hkv) >= kIntLimit)
         return LONGSPEC_HTA_ERR_INVALID_DIMS;
     if (D != 64 && D != 128) return LONGSPEC_HTA_ERR_UNSUPPORTED_D;
     HTA_TRY(check_rope(rope, D));

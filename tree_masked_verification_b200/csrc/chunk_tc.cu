@@ -67,19 +67,17 @@ constexpr int kPoisonRing = 6;
 #endif
 constexpr int kPolyEvery = HTA_POLY;               // one exp2 pair in this many on the FMA pipe (0: none)
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool ONE>
 struct Cfg {
-#ifndef HTA_NK
-#define HTA_NK 3
-#endif
-    static constexpr int NK = D == 128 ? HTA_NK : 4;             // K ring depth
-    static constexpr int NV = D == 128 ? 5 - HTA_NK : 4;             // V ring depth
+    // ring depths; with ONE row tile an item the second Q tile makes another stage
+    static constexpr int NK = D == 128 ? 3 : 4;
+    static constexpr int NV = (D == 128 ? 2 : 4) + (ONE ? 1 : 0);
     static constexpr int HALVES = D / 64;                   // 64-column swizzle boxes
     static constexpr int BOX = 128 * 64 * 2;
     static constexpr int TILE = 128 * D * 2;
     static constexpr int RAW = 128 * D;                     // a tile's codes, in the upper half of its stage
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = 2 * TILE;
+    static constexpr int OFF_K = (ONE ? 1 : 2) * TILE;
     static constexpr int OFF_V = OFF_K + NK * TILE;
     static constexpr int OFF_BAR = OFF_V + NV * TILE;
     // q_full, q_empty, o_full, o_empty, drain, k_full[NK], k_empty[NK], k_raw[NK], v_full[NV], v_empty[NV],
@@ -95,7 +93,7 @@ struct Cfg {
     static constexpr int OFF_EXP = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;   // per tile in flight: E of K, E of V
     static constexpr int OFF_RED = OFF_EXP + (Q8 ? kPoisonRing * 8 : 0);   // [2][4] words: a maximum over a loader set
     static constexpr int SMEM_ALLOC = OFF_RED + (Q8 ? 32 : 0);
-    static constexpr int OFF_XCH = TILE;                    // [2][3][128] floats, in the unused second Q tile
+    static constexpr int OFF_XCH = OFF_Q;                   // [2][3][128] floats: Q has been read by then
     static constexpr int OFF_PLAN = OFF_K;                  // int64 [kPlanUnits], before the first copy
     static constexpr int THREADS = Q8 ? 640 : 384;
     // registers per thread; the launch allots LAUNCH_REGS to each
@@ -239,12 +237,12 @@ __device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
 }  // namespace
 
 // ------------------------------------------------------------------- kernel
-template <int D, bool Q8>
-__global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
+template <int D, bool Q8, bool ONE>
+__global__ void __launch_bounds__(Cfg<D, Q8, ONE>::THREADS, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                 const __grid_constant__ ChunkParams p) {
-    using C = Cfg<D, Q8>;
+    using C = Cfg<D, Q8, ONE>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {                   // (the swizzled tiles need it; every slot is left empty)
@@ -442,7 +440,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         bool ok = true;
         w.start(p, s_start);
         while (ok && w.next(p)) {
-            const int two = w.it.two, n_steps = (w.j1 - w.j0) << two;
+            const int two = ONE ? 0 : w.it.two, n_steps = (w.j1 - w.j0) << two;
             int kw = 0;                             // K tiles of the item waited for
             auto qk = [&](int s) -> bool {          // scores of step s
                 const int g = s & 1, tile = s >> two;
@@ -580,18 +578,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         const bool live = row >= a && row < z;
                         const uint8_t *sc = is_v ? s_scale + C::NK * 256 + st * 128 : s_scale + st * 256;
                         const uint8_t *scv = is_v ? sc : sc + 128;
-                        read_row(stage);
                         const int e = sc[row], ev = scv[row];
                         const uint32_t e4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
-                        const uint32_t ev4 = *reinterpret_cast<const uint32_t *>(scv + 4 * lane);
                         const int E = tile_exp(e4, a, z);
                         if (!is_v) {
                             // V rows held as NaN, and V's E, are told to the softmax groups with K
                             const uint32_t nan = __ballot_sync(0xffffffffu, live && ev == kScaleNan);
-                            const int Ev = tile_exp(ev4, a, z);
+                            const int Ev = tile_exp(*reinterpret_cast<const uint32_t *>(scv + 4 * lane), a, z);
                             if (lane == 0) *word = nan;
                             if (first_thread) s_exp[at] = make_int2(E, Ev);
                         }
+                        read_row(stage);
                         write_row(stage, !live ? 0u : e != kScaleNan ? f16_pow2(min(e - E, 0)) : is_v ? 0u : 0x7e007e00u);
                     } else {
                         // tree rows (bf16), one a lane, scaled into f16 by the tile's largest value.
@@ -651,7 +648,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (first_thread) *more = w.next(p);
             bar_sync(1, 256);
             if (!*more) break;
-            const int two = w.it.two;
+            const int two = ONE ? 0 : w.it.two;
             const int row = two ? grp * 128 + r : r;        // row of the item
             const bool valid = row < w.it.rows;
             const bool warp_active = (two ? grp * 128 : 0) + wq * 32 < w.it.rows;
@@ -989,9 +986,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 // Rows of items that crossed CTA borders: the partials of an item are slot 1
 // of the CTA it begins in and slots 0 of the next n - 1.  One warp per row:
 //   out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M},  lse = M + ln(sum).
-// Bound by latency: the header, then all lse and the first eight partial
-// rows in one round of loads.
-template <int D>
+// Bound by latency: the header, then rounds of loads.  Few rows were split over
+// many CTAs (decode: eight segments at a time), many rows over two or three
+// (two segments of four rows at a time).
+template <int D, int R, int U>       // R rows of a warp and U segments at a time
 __global__ void __launch_bounds__(256)
 chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
     constexpr int DPL = D / 32;
@@ -1000,74 +998,86 @@ chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
     const PartHead hd = p.heads[2 * cta + 1];
     const int n = min(hd.n, p.grid - cta);
-    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < hd.rows; row += gridDim.y * 8) {
-        auto slot = [&](int i) { return slot_row(p, cta + i, i == 0 ? 1 : 0) + row; };
-        float ld[8][DPL];
-        auto load8 = [&](int i0) {
+    const float nan = __int_as_float(0x7fc00000);
+    for (int row0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R; row0 < hd.rows; row0 += gridDim.y * 8 * R) {
+        auto slot = [&](int i, int r) { return slot_row(p, cta + i, i == 0 ? 1 : 0) + min(row0 + r, hd.rows - 1); };
+        // one pass over the segments with running maxima
+        float m[R], sum[R], acc[R][DPL];
+        bool bad[R];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float *src = p.o_part + slot(min(i0 + u, n - 1)) * D + lane * DPL;
-                if constexpr (DPL == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src);
-                    ld[u][0] = x.x; ld[u][1] = x.y; ld[u][2] = x.z; ld[u][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(src);
-                    ld[u][0] = x.x; ld[u][1] = x.y;
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            sum[r] = 0.f;
+            bad[r] = false;
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) acc[r][k] = 0.f;
+        }
+        for (int i0 = 0; i0 < n; i0 += U) {
+            float ls[U][R], v[U][R][DPL];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const long long at = slot(min(i0 + u, n - 1), r);
+                    ls[u][r] = p.lse_part[at];
+                    const float *src = p.o_part + at * D + lane * DPL;
+                    if constexpr (DPL == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(src);
+                        v[u][r][0] = x.x; v[u][r][1] = x.y; v[u][r][2] = x.z; v[u][r][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2 *>(src);
+                        v[u][r][0] = x.x; v[u][r][1] = x.y;
+                    }
+                }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mn = m[r];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    bad[r] |= ls[u][r] != ls[u][r];
+                    if (i0 + u >= n) ls[u][r] = -INFINITY;
+                    mn = fmaxf(mn, ls[u][r]);
+                }
+                if (mn == -INFINITY) continue;          // (no visible key so far)
+                const float a = ex2((m[r] - mn) * kLog2e);
+                m[r] = mn;
+                sum[r] *= a;
+#pragma unroll
+                for (int k = 0; k < DPL; ++k) acc[r][k] *= a;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float w = ex2((ls[u][r] - mn) * kLog2e);
+                    if (w == 0.f) continue;             // (a segment without visible keys, or none)
+                    sum[r] += w;
+#pragma unroll
+                    for (int k = 0; k < DPL; ++k) acc[r][k] = fmaf(w, v[u][r][k], acc[r][k]);
                 }
             }
-        };
-        load8(0);
-        float mx = -INFINITY, mine = -INFINITY;
-        bool bad = false;
-        for (int i = lane; i < n; i += 32) {
-            const float v = p.lse_part[slot(i)];
-            if (i < 32) mine = v;
-            bad |= v != v;
-            mx = fmaxf(mx, v);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        bad = __any_sync(0xffffffffu, bad);
-        float acc[DPL], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            if (i0 > 0) {
-                load8(i0);
-                if (i0 % 32 == 0) mine = i0 + lane < n ? p.lse_part[slot(i0 + lane)] : -INFINITY;
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= hd.rows) break;
+            const float inv = bad[r] ? nan : sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+            const float lse = bad[r] ? nan : sum[r] > 0.f ? m[r] + lg2(sum[r]) * kLn2 : -INFINITY;
+            const int pr = hd.r0 + row0 + r;
+            size_t orow;
+            if (p.tree) {
+                orow = (static_cast<size_t>(hd.b) * p.Hq + static_cast<size_t>(hd.kvh) * p.G) * p.N + pr;
+            } else {
+                const int t = div_g(p, pr);
+                orow = static_cast<size_t>(hd.s0 + t) * p.Hq + hd.kvh * p.G + (pr - t * p.G);
             }
-            const float wgt = mx == -INFINITY ? 0.f : ex2((mine - mx) * kLog2e);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float wi = __shfl_sync(0xffffffffu, wgt, (i0 + u) & 31);
-                if (i0 + u < n && wi > 0.f) {   // (a segment without visible keys weighs nothing)
-                    sum += wi;
-#pragma unroll
-                    for (int k = 0; k < DPL; ++k) acc[k] = fmaf(wi, ld[u][k], acc[k]);
-                }
+            __nv_bfloat16 *dst = p.out + orow * D + lane * DPL;
+            if constexpr (DPL == 4) {
+                uint2 pk;
+                pk.x = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
+                pk.y = pack_bf16x2(acc[r][2] * inv, acc[r][3] * inv);
+                *reinterpret_cast<uint2 *>(dst) = pk;
+            } else {
+                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
             }
+            if (lane == 0) p.lse[orow] = lse;
         }
-        const float nan = __int_as_float(0x7fc00000);
-        const float inv = bad ? nan : sum > 0.f ? 1.f / sum : 0.f;
-        const float lse = bad ? nan : sum > 0.f ? mx + lg2(sum) * kLn2 : -INFINITY;
-        const int pr = hd.r0 + row;
-        size_t orow;
-        if (p.tree) {
-            orow = (static_cast<size_t>(hd.b) * p.Hq + static_cast<size_t>(hd.kvh) * p.G) * p.N + pr;
-        } else {
-            const int t = div_g(p, pr);
-            orow = static_cast<size_t>(hd.s0 + t) * p.Hq + hd.kvh * p.G + (pr - t * p.G);
-        }
-        __nv_bfloat16 *dst = p.out + orow * D + lane * DPL;
-        if constexpr (DPL == 4) {
-            uint2 pk;
-            pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-            pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-            *reinterpret_cast<uint2 *>(dst) = pk;
-        } else {
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        }
-        if (lane == 0) p.lse[orow] = lse;
     }
 }
 
@@ -1079,25 +1089,29 @@ cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = stream;
-    // (eight blocks of eight rows per CTA make one wave)
-    cfg.gridDim = dim3(p.grid, min(8, (p.slot_rows + 7) / 8));
     cfg.blockDim = dim3(256);
-    return p.D == 128 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128>, p)
-                      : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64>, p);
+    if (p.slot_rows <= 16) {
+        cfg.gridDim = dim3(p.grid, (p.slot_rows + 7) / 8);
+        return p.D == 128 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128, 1, 8>, p)
+                          : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64, 1, 8>, p);
+    }
+    cfg.gridDim = dim3(p.grid, (p.slot_rows + 31) / 32);
+    return p.D == 128 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128, 4, 2>, p)
+                      : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64, 4, 2>, p);
 }
 
 namespace {
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool ONE>
 cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream) {
-    using C = Cfg<D, Q8>;
+    using C = Cfg<D, Q8, ONE>;
     constexpr int kMaxDev = 64;
     static bool attr_set[kMaxDev] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDev || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+        e = cudaFuncSetAttribute(chunk_tc_kernel<D, Q8, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
     }
@@ -1111,7 +1125,7 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8>, tm[0], tm[1], tm[2], tm[3], p);
+    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8, ONE>, tm[0], tm[1], tm[2], tm[3], p);
     if (e != cudaSuccess) return e;
     return launch_chunk_merge(p, stream);
 }
@@ -1120,14 +1134,25 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
 
 cudaError_t launch_chunk_tc(const ChunkParams &p0, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     ChunkParams p = p0;
-    p.item_rows = 256;
-    p.c0 = 4;
+    // One row tile an item where sequences have at most one on average: deeper
+    // rings for what is then bound by the keys' way to the SM.
+    const bool one = p.tree ? 1LL * p.N * p.G <= 128 : 1LL * p.N * p.G <= 128LL * p.B;
+    p.item_rows = one ? 128 : 256;
+    p.slot_rows = p.slot_rows < p.item_rows ? p.slot_rows : p.item_rows;
+    // An item's own time (its queries' way in, its rows' way out, the pipeline's
+    // fill) is that of about two key tiles (ragged windowed chunks: 67 us with a
+    // half, 61 with two).
+    p.c0 = 18;
     p.c1 = 4;
     p.c2 = 8;
     p.min_share = 8;
     const bool q8 = p.cache.k_scale != nullptr;
-    if (p.D == 128) return q8 ? launch<128, true>(p, tm, stream) : launch<128, false>(p, tm, stream);
-    return q8 ? launch<64, true>(p, tm, stream) : launch<64, false>(p, tm, stream);
+    if (p.D == 128) {
+        if (one) return q8 ? launch<128, true, true>(p, tm, stream) : launch<128, false, true>(p, tm, stream);
+        return q8 ? launch<128, true, false>(p, tm, stream) : launch<128, false, false>(p, tm, stream);
+    }
+    if (one) return q8 ? launch<64, true, true>(p, tm, stream) : launch<64, false, true>(p, tm, stream);
+    return q8 ? launch<64, true, false>(p, tm, stream) : launch<64, false, false>(p, tm, stream);
 }
 
 }  // namespace hta
