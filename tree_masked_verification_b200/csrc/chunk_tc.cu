@@ -62,10 +62,11 @@ namespace {
 // NaN words of the tiles in flight: K of tile p is there at the earliest when
 // the softmax of tile p - NK - 2 is done, so NK + 2 places are enough
 constexpr int kPoisonRing = 6;
-#ifndef HTA_POLY
-#define HTA_POLY 4
-#endif
-constexpr int kPolyEvery = HTA_POLY;               // one exp2 pair in this many on the FMA pipe (0: none)
+// One exp2 pair in this many on the FMA pipe (0: none).  Prefill of 4k behind
+// 12k: 1.62 M cycles a CTA with none, 1.52 with one in 8, 1.50 with one in 4, 1.47
+// with one in 2, which the e4m3 kernel's busier schedulers pay for (a tree over
+// 32k keys: 111 us with one in 4, 126 with one in 2).
+constexpr int kPolyEvery = 4;
 
 template <int D, bool Q8, bool ONE>
 struct Cfg {
@@ -98,8 +99,8 @@ struct Cfg {
     static constexpr int THREADS = Q8 ? 640 : 384;
     // registers per thread; the launch allots LAUNCH_REGS to each
     static constexpr int LAUNCH_REGS = Q8 ? 96 : 168;
-    static constexpr int REGS_SOFTMAX = Q8 ? 136 : 224;
-    static constexpr int REGS_LOAD = 72;
+    static constexpr int REGS_SOFTMAX = Q8 ? 120 : 224;
+    static constexpr int REGS_LOAD = 88;
     static constexpr int REGS_OTHER = Q8 ? 64 : 56;
     static_assert(256 * REGS_SOFTMAX + (Q8 ? 256 * REGS_LOAD : 0) + 128 * REGS_OTHER <= THREADS * LAUNCH_REGS,
                   "register split must fit the launch allocation");
@@ -210,10 +211,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // 2^x for a pair on the FMA pipe (part of the load off the exp2 unit): n =
-// round(x) by the 1.5 * 2^23 addition, 2^(x - n) by the cubic fitted in
-// fit_exp2_poly.py (relative 7.5e-5), n into the exponent.  x is clamped to
-// >= -125: 2^-125 is nothing beside the row's largest term (and a row that
-// sees no key is recognised by its maximum, not by its sum).
+// round(x) by the 1.5 * 2^23 addition, 2^(x - n) by the quartic fitted in
+// fit_exp2_poly.py (relative 2.7e-6: the lse, an fp32 result, shows it), n into
+// the exponent.  x is clamped to >= -125: 2^-125 is nothing beside the row's
+// largest term (and a row that sees no key is recognised by its maximum, not
+// by its sum).
 __device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
     constexpr float kRound = 12582912.0f;
     float2 v = unf2(x2);
@@ -223,10 +225,11 @@ __device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
     const uint64_t t = add2(xc, f2(kRound, kRound));
     const uint64_t n = add2(t, f2(-kRound, -kRound));
     const uint64_t fr = fma2(n, f2(-1.f, -1.f), xc);
-    uint64_t q = fma2(fr, f2(0.05517132207751274f, 0.05517132207751274f),
-                      f2(0.24261054396629333f, 0.24261054396629333f));
-    q = fma2(fr, q, f2(0.6932609677314758f, 0.6932609677314758f));
-    q = fma2(fr, q, f2(0.9999281167984009f, 0.9999281167984009f));
+    uint64_t q = fma2(fr, f2(0.009570068679749966f, 0.009570068679749966f),
+                      f2(0.055917806923389435f, 0.055917806923389435f));
+    q = fma2(fr, q, f2(0.240247443318367f, 0.240247443318367f));
+    q = fma2(fr, q, f2(0.6931218504905701f, 0.6931218504905701f));
+    q = fma2(fr, q, f2(0.9999992847442627f, 0.9999992847442627f));
     const float2 qq = unf2(q), tt = unf2(t);
     float2 o;
     o.x = __int_as_float(__float_as_int(qq.x) + (__float_as_int(tt.x) << 23));
@@ -844,26 +847,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         uint32_t x[32], pk[16];
                         tmem_ld32(t_s + 32 * q, x);
                         tmem_wait_ld();
-                        float2 e[16];
+                        uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const uint64_t x2 = fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, nm);
+                            float2 e;
                             if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
-                                e[k] = exp2_poly2(x2);
+                                e = exp2_poly2(x2);
                             } else {
                                 const float2 y = unf2(x2);
-                                e[k] = make_float2(ex2(y.x), ex2(y.y));
+                                e = make_float2(ex2(y.x), ex2(y.y));
                             }
+                            pk[k] = Q8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                            ls[k & 1] = add2(ls[k & 1], f2(e.x, e.y));
                         }
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) pk[k] = Q8 ? pack_f16x2(e[k].x, e[k].y) : pack_bf16x2(e[k].x, e[k].y);
-                        uint64_t la = f2(e[0].x, e[0].y), lb = f2(e[1].x, e[1].y);
-#pragma unroll
-                        for (int k = 2; k < 16; k += 2) {
-                            la = add2(la, f2(e[k].x, e[k].y));
-                            lb = add2(lb, f2(e[k + 1].x, e[k + 1].y));
-                        }
-                        lt = add2(lt, add2(la, lb));
+                        lt = add2(lt, add2(ls[0], ls[1]));
                         // P of these 32 keys on 16 columns whose scores have been read
                         tmem_st16(t_s + 16 * q, pk);
                         if (q & 1) {
