@@ -9,11 +9,10 @@
 //   max|x| <= 448 * 2^(e - 127),  e clamped to [16, 134].
 // A power of two costs an e4m3 row nothing that a free scale would save (the
 // codes are floating point: their relative spacing does not move, only the
-// 18-octave range shifts by less than one octave), and it makes c * 2^k
-// exactly representable in bf16, so that the attention kernels feed the
-// dequantised rows to bf16 tensor-core products without a rounding.  The upper
-// clamp keeps the kernels' one multiplication by 2^(e - 7) in bf16's range;
-// values above 448 * 2^7 = 57344 saturate there.  A row holding a NaN or an
+// 18-octave range shifts by less than one octave), and the attention kernels
+// can then scale codes exactly: they feed f16 tensor-core products, in which
+// every code and every value the format holds (up to 448 * 2^7 = 57344, the
+// upper clamp; larger ones saturate) is a number.  A row holding a NaN or an
 // infinity is stored as e = 255 with NaN codes and reads back as NaN.
 #pragma once
 

@@ -12,35 +12,50 @@
 // K/V tile they read (one tile when at most 128 rows are left).  An item's
 // keys come in tiles of 128.
 //
-// Schedule.  Lengths are known to the device only, so every CTA (one per SM)
-// computes the work of all items in units (c0 + tiles * c1 or c2) and takes
-// an equal, contiguous range of the whole: long axes are split over as many
-// CTAs as it takes and ragged batches balance, without a plan kernel or a
-// host copy.  An item that lies in one CTA's range is finished there; one
-// that crosses a border leaves normalised fp32 partials and their lse, at
-// most two per CTA (its first and its last item), which merge_kernel joins.
+// Schedule (chunk_plan.cuh).  Lengths are known to the device only, so every
+// CTA (one per SM) computes the work of all items and takes an equal,
+// contiguous range of the whole: long axes are split over as many CTAs as it
+// takes and ragged batches balance, without a plan kernel or a host copy.  An
+// item that lies in one CTA's range is finished there; one that crosses a
+// border leaves normalised fp32 partials and their lse, at most two per CTA
+// (its first and its last item), which chunk_merge_kernel joins.  Nothing
+// depends on the order in which CTAs run.
 //
 // Warps: 0 TMA producer of K, 1 MMA issuer, 2 TMA producer of V, 3 fixer of
 // partly visible V tiles (bf16 caches), 4-7 and 8-11 two softmax groups (one
-// row per thread), 12-19 loaders (e4m3 caches).  TMA leaves a tile's codes in
-// the upper half of its stage; the loaders read them into registers and write
-// the whole stage over as the swizzled f16 tile the MMAs read, so that codes
-// need no buffers of their own and the rings prefetch as deep as for bf16.
-// (Loads straight into registers, one tile ahead, took 5 us a tile: a warp's
-// waits on them cover younger loads too, so that each tile waited for the
-// next one's.)  e4m3 caches run the MMAs in f16: a code is one of f16's
-// numbers, two to a conversion, where bf16 took ten integer operations for
-// four and the integer pipe was the bound.  A tile's rows are scaled to its
-// largest scale E (rows 2^-24 below it vanish beside it), 2^(E - 127) goes to
-// the scores, or for V to the weights: against a running reference E_run, by
-// which the output is multiplied at the end.  E is at least 96 (V of 1e-7: an
-// all-zero tile must not drive the weights out of fp32's range).  Query rows
-// are scaled by powers of two into f16, which holds bf16's 8 bits down to
-// 2^-28 of the row's largest value.  With two
-// row tiles group g owns tile g and runs every key tile; with one, group g runs the key tiles j = g mod 2 into
-// an accumulator of its own and the two are merged at the end (the lse merge
-// of two key ranges).  Steps s of an item: group s & 1, key tile
-// s >> (two row tiles); MMA order QK_0 QK_1 [PV_0 QK_2] [PV_1 QK_3] ...
+// row per thread), 12-15 and 16-19 loaders of K and of V (e4m3 caches).  With
+// two row tiles group g owns tile g and runs every key tile; with one, group g
+// runs the key tiles j = g mod 2 into an accumulator of its own and the two are
+// merged at the end (the lse merge of two key ranges).  Steps s of an item:
+// group s & 1, key tile s >> (two row tiles); MMA order QK_0 QK_1 [PV_0 QK_2]
+// [PV_1 QK_3] ..., P*V in two halves of the keys, the first while the softmax
+// group works on the second (prefill 990 -> 963 us).
+//
+// e4m3 caches.  TMA leaves a tile's codes in the upper half of its stage; a
+// loader reads its row into registers and writes it back over the whole stage
+// as the swizzled f16 tile the MMAs read, so that codes need no buffers of
+// their own and the rings prefetch as deep as for bf16.  (Loads straight into
+// registers, one tile ahead, took 5 us a tile: a warp's waits on them cover
+// younger loads too, so that each tile waited for the next one's.)  The MMAs
+// run in f16: every code is one of f16's numbers, and two conversions and two
+// products make four of them where bf16 takes ten instructions.  A tile's
+// rows are scaled to its largest scale E (rows 2^-24 below it vanish beside
+// it); 2^(E - 127) goes to the scores, or for V to the weights, against a
+// running reference e_run by which the output is multiplied at the end.  E is
+// at least 96 (values of 2e-7): an all-zero tile must not drive the weights
+// out of fp32's range.  Query rows are scaled by powers of two into f16, which
+// holds bf16's 8 bits down to 2^-28 of the row's largest value.
+//
+// Measured (B200, 1965 MHz under the power cap): prefill of 4096 tokens behind
+// 12288, 32 heads over 8: 0.96-1.0 ms, 970-1000 TFLOP/s, 0.6 of cuBLAS's rate.  A
+// pair of 128 x 128 tiles takes 3.8 k cycles against 2048 of MMA: a group's
+// chain is 1.95 k of softmax, the MMAs of the next scores behind it (1.0 k) and
+// about 0.8 k of hand-over, and two groups fill it to 54 %.  The exp2 unit shows in it
+// (kPolyEvery), the MMA issue does not (70 cycles for eight).  Decode of 16
+// sequences, bf16: 208 us, 6.0 TB/s, 0.92 of the measured copy.  A 68-node tree
+// over e4m3 keys, 8 x 32 heads: 318 us, 2.5 TB/s of codes: 3.0 k cycles a
+// 128-key tile, of which the conversion's traffic in shared memory beside the
+// MMAs' own costs 0.6 k (without it 2.4 k).
 //
 // Tensor memory: S[g] columns 128g.. (fp32 scores; P as 16-bit pairs over its
 // first 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
@@ -534,9 +549,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // A stage's codes to f16, in place, times the row's `mult` (0: zeros).  At
             // D = 128 a row's codes lie where its own second half goes, so a lane needs
             // no other's progress; at D = 64 they lie where other warps' rows go.  All
-            // loads of the row first: beside the tensor-memory traffic a load from shared
-            // memory takes hundreds of cycles (four at a time, with the multipliers by
-            // shuffles: 2400 cycles a tile).
+            // loads of the row first: beside the MMAs' traffic a load from shared memory
+            // takes hundreds of cycles (four at a time, with the multipliers by shuffles:
+            // 2400 cycles a tile against 1100).
             uint2 u[D / 8];
             auto read_row = [&](const uint8_t *stage) {
 #pragma unroll
@@ -781,10 +796,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         }
                         shift = static_cast<float>(E.y - e_run);
                     }
-                    // Three short loops over the row's 128 scores, 32 at a time, from
-                    // tensor memory each time: the code stays small.  (Unrolled over all
-                    // 128 it was fetched, not issued, at the pace the five roles that
-                    // share a scheduler left: see the figures above.)
+                    // Passes over the row's 128 scores, 32 at a time, from tensor memory each
+                    // time: hidden keys to -inf (partly visible tiles), the maximum, the
+                    // weights.  One pass with all 128 in registers took the same time (983
+                    // against 990 us for the prefill) and left the e4m3 loaders too few.
                     if (masked) {
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
