@@ -525,10 +525,11 @@ LONGSPEC_HTA_API int longspec_hta_append_paged(const longspec_hta_dims *dims, co
  * when window > 0.  One token per sequence is a decode step, a whole prompt
  * a prefill, and ragged chunks mix both in one call.
  *   dims: B, Hq, Hkv, D, L_cap, scale, T = N tokens (as in append);
- *   q: rows of Hq heads (stride_b not used, stride_h must be D);
+ *   q: rows of Hq heads (stride_b not used, stride_h must be D where Hq > 1);
  *   out bf16 [N][Hq][D], lse fp32 [N][Hq] (natural log);
  *   workspace: longspec_hta_chunk_workspace_bytes(dims) bytes, 16-byte
- *   aligned, status word first.
+ *   aligned, status word first; calls that can overlap on the GPU need
+ *   workspaces of their own.
  * Cache rows outside a sequence's keys, and table entries of blocks that
  * hold none of the keys its tokens see, are not read as keys (they may hold
  * anything).  Padding tokens' rows of out and lse are left as they are.

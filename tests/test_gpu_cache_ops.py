@@ -642,3 +642,16 @@ def test_workspaces_and_devices_are_checked():
     with pytest.raises(hta.HtaError) as e:
         hta.chunk_attention_paged(c.q, c.kc, c.vc, c.table, c.prefix_len, c.q_start, window=-1, **c.paged())
     assert e.value.code == hta.ERR_INVALID_OPTION
+
+
+def test_one_head_at_any_stride():
+    """A single query head of wider rows; a single token of wider rows."""
+    c = Case([50, 9], [7, 1], 1, 1, 128, 16, seed=4)
+    want, want_lse, _ = c.attend()
+    wide = torch.zeros((c.N, 4, 128), dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:3] = c.q
+    c.q = wide[:, 2:3]
+    out, lse, code = c.attend()
+    assert code == hta.OK and torch.equal(out, want) and torch.equal(lse, want_lse)
+    c.q = wide[:, 2].unsqueeze(1).transpose(0, 1).transpose(0, 1)
+    assert torch.equal(c.attend()[0], want)

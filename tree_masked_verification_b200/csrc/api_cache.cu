@@ -247,7 +247,7 @@ int longspec_hta_chunk_attention_paged(const longspec_hta_dims *dims, const long
     HTA_TRY(check_workspace(workspace, workspace_bytes, hta::kStatusBytes));
     if (dims->T == 0) return LONGSPEC_HTA_OK;
     HTA_TRY(check_heads(q));
-    if (q->stride_h != dims->D) return LONGSPEC_HTA_ERR_INVALID_OPTION;
+    if (dims->Hq > 1 && q->stride_h != dims->D) return LONGSPEC_HTA_ERR_INVALID_OPTION;
     if (!out || !lse) return LONGSPEC_HTA_ERR_NULL_POINTER;
     if (!aligned16(out) || !aligned4(lse)) return LONGSPEC_HTA_ERR_MISALIGNED;
     DeviceInfo di;

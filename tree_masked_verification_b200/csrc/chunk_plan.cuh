@@ -162,15 +162,15 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
                 return past != 0;
             };
             int k = 0, u = 0;
-            while (!find(u + lane < units ? plan[u + lane] * p.Hkv : 0, k)) u += 32;
-            u += k;
+            while (!find(u + lane < units ? plan[u + lane] * p.Hkv : 0, k) && u < units) u += 32;
+            u = min(u + k, units - 1);
             st.b = u;
             long long cost = plan[u];
             if (per == 32) {
                 const int b = u * 32 + lane;
                 const long long c = b < p.B ? seq_cost(p, load_seq(p, b), 0, 1) : 0;
                 find(c * p.Hkv, k);
-                st.b = u * 32 + k;
+                st.b = min(u * 32 + k, p.B - 1);
                 cost = __shfl_sync(0xffffffffu, c, k);
             }
             const Seq s = load_seq(p, st.b);
@@ -178,7 +178,10 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
             if ((st.kvh + 1) * cost <= begin - before) ++st.kvh;     // (the division's rounding)
             if (st.kvh * cost > begin - before) --st.kvh;
             before += cost * st.kvh;
-            while (!find(st.tile + lane < s.tiles ? item_cost(p, item_of(p, s, st.tile + lane)) : 0, k)) st.tile += 32;
+            // (bounded: lengths that another stream changed meanwhile must not hang the search)
+            while (!find(st.tile + lane < s.tiles ? item_cost(p, item_of(p, s, st.tile + lane)) : 0, k) &&
+                   st.tile < s.tiles)
+                st.tile += 32;
             st.tile += k;
             st.at = before;
         }

@@ -652,7 +652,10 @@ def _heads(t, name, dev: int, b, n, h):
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    return _heads_struct(t.data_ptr(), 0 if b < 0 else st[b], st[n], st[h])
+    sb, sn, sh = 0 if b < 0 else st[b], st[n], st[h]
+    if (sb | sn | sh) & 7:           # (the stride of an axis of one means nothing)
+        sb, sn, sh = (x if t.shape[i] > 1 else 0 for x, i in ((sb, b), (sn, n), (sh, h)))
+    return _heads_struct(t.data_ptr(), sb, sn, sh)
 
 
 def _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev: int) -> Rope:
@@ -813,7 +816,7 @@ def chunk_attention_paged(q, k_cache, v_cache, block_table, prefix_len, q_start,
     cache = _cache(k_cache, v_cache, block_table, k_scale, v_scale, dev)
     B, pre, start = _ragged(prefix_len, q_start, block_table, dev)
     st = _stream_on(dev, stream)
-    if q.stride(1) != D:
+    if Hq > 1 and q.stride(1) != D:
         raise ValueError("q: the heads of a token must be contiguous")
     out = torch.empty_like(q, memory_format=_contiguous) if out is None else _result(out, "out", shape, _BF16, dev)
     lse = (q.new_empty((N, Hq), dtype=torch.float32) if lse is None
