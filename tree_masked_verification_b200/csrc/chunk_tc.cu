@@ -495,16 +495,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const uint64_t vd = vdesc + ((vst * C::TILE) >> 4);
                 const bool done = !two || g == 1;
                 auto pv = [&](int kk) {
-                    mma_ts(tmem + C::COL_O + g * D, tmem + C::COL_S + g * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4), C::IDESC_PV,
-                           (s > 1 || kk > 0) ? 1u : 0u);
+                    mma_ts(tmem + C::COL_O + g * D, tmem + C::COL_S + g * 128 + 64 + kk * 8, vd + ((kk * 16 * 128) >> 4), C::IDESC_PV,
+                           (s > 1 || kk != 4) ? 1u : 0u);
                 };
-                // the first 64 keys while the softmax group works on the others
+                // the upper 64 keys while the softmax group works on the lower ones
                 if (ok) ok = warp_wait(p_ready + 2 * g, g ? cnt1 : cnt0);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) pv(kk);
+                    for (int kk = 4; kk < 8; ++kk) pv(kk);
                 }
                 ok = warp_wait(p_ready + 2 * g + 1, g ? cnt1 : cnt0);
                 if (!ok) break;
@@ -512,7 +512,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 4; kk < 8; ++kk) pv(kk);
+                    for (int kk = 0; kk < 4; ++kk) pv(kk);
                     if (done) mma_commit(v_empty + vst);
                     if (s == n_steps - 1) mma_commit(o_full);
                 }
@@ -814,22 +814,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         tmem_wait_st();
                     }
                     float mt = -INFINITY;
-                    {
-                        uint32_t x[2][32];
-                        tmem_ld32(t_s, x[0]);
+                    uint32_t x[2][32];                  // two quarters, the next on its way
+                    tmem_ld32(t_s, x[0]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tmem_wait_ld();
-                            pin(x[q & 1]);
-                            if (q < 3) tmem_ld32(t_s + 32 * (q + 1), x[(q + 1) & 1]);
-                            float a = -INFINITY, b2 = -INFINITY;
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_wait_ld();
+                        pin(x[q & 1]);
+                        if (q < 3) tmem_ld32(t_s + 32 * (q + 1), x[(q + 1) & 1]);
+                        float a = -INFINITY, b2 = -INFINITY;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                a = max3(a, __uint_as_float(x[q & 1][i]), __uint_as_float(x[q & 1][i + 1]));
-                                b2 = max3(b2, __uint_as_float(x[q & 1][i + 2]), __uint_as_float(x[q & 1][i + 3]));
-                            }
-                            mt = max3(mt, a, b2);
+                        for (int i = 0; i < 32; i += 4) {
+                            a = max3(a, __uint_as_float(x[q & 1][i]), __uint_as_float(x[q & 1][i + 1]));
+                            b2 = max3(b2, __uint_as_float(x[q & 1][i + 2]), __uint_as_float(x[q & 1][i + 3]));
                         }
+                        mt = max3(mt, a, b2);
                     }
                     const float m_tile = mt * c2;
                     if (m_tile != m_tile) row_nan = true;
@@ -857,37 +855,57 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const float mu = (m_run == -INFINITY ? 0.f : m_run) - shift;
                     const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
                     uint64_t lt = 0;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t x[32], pk[16];
-                        tmem_ld32(t_s + 32 * q, x);
-                        tmem_wait_ld();
+                    // From the last quarter to the first (bf16: the last two are in registers
+                    // still): P of quarter q on the columns 64 + 16q .., whose scores have
+                    // been read by then.
+                    auto weights = [&](const uint32_t (&y)[32], int q) {
+                        uint32_t pk[16];
                         uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const uint64_t x2 = fma2(f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, nm);
+                            const uint64_t x2 = fma2(f2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), cc, nm);
                             float2 e;
                             if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
                                 e = exp2_poly2(x2);
                             } else {
-                                const float2 y = unf2(x2);
-                                e = make_float2(ex2(y.x), ex2(y.y));
+                                const float2 z = unf2(x2);
+                                e = make_float2(ex2(z.x), ex2(z.y));
                             }
                             pk[k] = Q8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                             ls[k & 1] = add2(ls[k & 1], f2(e.x, e.y));
                         }
                         lt = add2(lt, add2(ls[0], ls[1]));
-                        // P of these 32 keys on 16 columns whose scores have been read
-                        tmem_st16(t_s + 16 * q, pk);
-                        if (q & 1) {
-                            tmem_wait_st();
-                            if (q == 1) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(p_ready + 2 * grp);
-                            }
+                        tmem_st16(t_s + 64 + 16 * q, pk);
+                    };
+                    auto half_done = [&]() {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_ready + 2 * grp);
+                    };
+                    if constexpr (!Q8) {
+                        weights(x[1], 3);
+                        tmem_ld32(t_s + 32, x[1]);
+                        weights(x[0], 2);
+                        tmem_ld32(t_s, x[0]);
+                        half_done();
+                        tmem_wait_ld();
+                        pin(x[1]);
+                        pin(x[0]);
+                        weights(x[1], 1);
+                        weights(x[0], 0);
+                    } else {                            // (as a loop: fewer registers)
+#pragma unroll 1
+                        for (int q = 3; q >= 0; --q) {
+                            uint32_t y[32];
+                            tmem_ld32(t_s + 32 * q, y);
+                            tmem_wait_ld();
+                            pin(y);
+                            weights(y, q);
+                            if (q == 2) half_done();
                         }
                     }
+                    tmem_wait_st();
                     if constexpr (Q8) {
                         const float back = ex2(-shift);
                         l2 = fma2(lt, f2(back, back), l2);
