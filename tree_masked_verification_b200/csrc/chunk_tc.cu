@@ -46,16 +46,16 @@
 // out of fp32's range.  Query rows are scaled by powers of two into f16, which
 // holds bf16's 8 bits down to 2^-28 of the row's largest value.
 //
-// Measured (B200, 1965 MHz under the power cap): prefill of 4096 tokens behind
-// 12288, 32 heads over 8: 0.96-1.0 ms, 970-1000 TFLOP/s, 0.6 of cuBLAS's rate.  A
-// pair of 128 x 128 tiles takes 3.8 k cycles against 2048 of MMA: a group's
-// chain is 1.95 k of softmax, the MMAs of the next scores behind it (1.0 k) and
-// about 0.8 k of hand-over, and two groups fill it to 54 %.  The exp2 unit shows in it
-// (kPolyEvery), the MMA issue does not (70 cycles for eight).  Decode of 16
-// sequences, bf16: 208 us, 6.0 TB/s, 0.92 of the measured copy.  A 68-node tree
-// over e4m3 keys, 8 x 32 heads: 318 us, 2.5 TB/s of codes: 3.0 k cycles a
-// 128-key tile, of which the conversion's traffic in shared memory beside the
-// MMAs' own costs 0.6 k (without it 2.4 k).
+// Measured (B200, 1965 MHz, at the power cap in long runs): prefill of 4096
+// tokens behind 12288, 32 heads over 8: 0.95 ms, 1.0 PFLOP/s, 0.62 of cuBLAS's
+// rate.  A pair of 128 x 128 tiles takes 3.7 k cycles against 2048 of MMA: the
+// chain of a group is its softmax (1.9 k), the MMAs of the next scores behind it
+// (1.0 k) and hand-overs, and two groups fill the MMAs to 55-60 %; issuing eight
+// MMAs takes 70 cycles, and no pipe is above 45 %.  Decode of 16 sequences, bf16:
+// 205-215 us, 0.88-0.93 of the measured copy.  A 68-node tree over e4m3 keys,
+// 8 x 32 heads: 307 us, 2.6 TB/s of codes: 3.0 k cycles a 128-key tile, of which
+// the conversion's traffic in shared memory beside the MMAs' own costs 0.6 k
+// (without it 2.4 k).
 //
 // Tensor memory: S[g] columns 128g.. (fp32 scores; P as 16-bit pairs over its
 // first 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
@@ -77,11 +77,6 @@ namespace {
 // NaN words of the tiles in flight: K of tile p is there at the earliest when
 // the softmax of tile p - NK - 2 is done, so NK + 2 places are enough
 constexpr int kPoisonRing = 6;
-// One exp2 pair in this many on the FMA pipe (0: none).  Prefill of 4k behind
-// 12k: 1.62 M cycles a CTA with none, 1.52 with one in 8, 1.50 with one in 4, 1.47
-// with one in 2, which the e4m3 kernel's busier schedulers pay for (a tree over
-// 32k keys: 111 us with one in 4, 126 with one in 2).
-constexpr int kPolyEvery = 4;
 
 template <int D, bool Q8, bool ONE>
 struct Cfg {
@@ -223,33 +218,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// 2^x for a pair on the FMA pipe (part of the load off the exp2 unit): n =
-// round(x) by the 1.5 * 2^23 addition, 2^(x - n) by the quartic fitted in
-// fit_exp2_poly.py (relative 2.7e-6: the lse, an fp32 result, shows it), n into
-// the exponent.  x is clamped to >= -125: 2^-125 is nothing beside the row's
-// largest term (and a row that sees no key is recognised by its maximum, not
-// by its sum).
-__device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
-    constexpr float kRound = 12582912.0f;
-    float2 v = unf2(x2);
-    v.x = fmaxf(v.x, -125.f);
-    v.y = fmaxf(v.y, -125.f);
-    const uint64_t xc = f2(v.x, v.y);
-    const uint64_t t = add2(xc, f2(kRound, kRound));
-    const uint64_t n = add2(t, f2(-kRound, -kRound));
-    const uint64_t fr = fma2(n, f2(-1.f, -1.f), xc);
-    uint64_t q = fma2(fr, f2(0.009570068679749966f, 0.009570068679749966f),
-                      f2(0.055917806923389435f, 0.055917806923389435f));
-    q = fma2(fr, q, f2(0.240247443318367f, 0.240247443318367f));
-    q = fma2(fr, q, f2(0.6931218504905701f, 0.6931218504905701f));
-    q = fma2(fr, q, f2(0.9999992847442627f, 0.9999992847442627f));
-    const float2 qq = unf2(q), tt = unf2(t);
-    float2 o;
-    o.x = __int_as_float(__float_as_int(qq.x) + (__float_as_int(tt.x) << 23));
-    o.y = __int_as_float(__float_as_int(qq.y) + (__float_as_int(tt.y) << 23));
-    return o;
 }
 
 }  // namespace
@@ -855,6 +823,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const float mu = (m_run == -INFINITY ? 0.f : m_run) - shift;
                     const uint64_t cc = f2(c2, c2), nm = f2(-mu, -mu);
                     uint64_t lt = 0;
+                    // (All exponentials on the exp2 unit: a polynomial on the FMA pipe for one
+                    // in 2, 4, 5 or 8 of them was 1 to 4 % slower for the prefill.)
                     // From the last quarter to the first (bf16: the last two are in registers
                     // still): P of quarter q on the columns 64 + 16q .., whose scores have
                     // been read by then.
@@ -864,13 +834,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const uint64_t x2 = fma2(f2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), cc, nm);
-                            float2 e;
-                            if (kPolyEvery > 0 && k % kPolyEvery == kPolyEvery - 1) {
-                                e = exp2_poly2(x2);
-                            } else {
-                                const float2 z = unf2(x2);
-                                e = make_float2(ex2(z.x), ex2(z.y));
-                            }
+                            const float2 z = unf2(x2), e = make_float2(ex2(z.x), ex2(z.y));
                             pk[k] = Q8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                             ls[k & 1] = add2(ls[k & 1], f2(e.x, e.y));
                         }

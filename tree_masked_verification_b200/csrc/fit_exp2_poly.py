@@ -1,13 +1,11 @@
-"""Fits of the polynomials used for part of the exp2 evaluations: the cubic of
-prefix_tc.cu and the quartic of chunk_tc.cu.
+"""Fit of the cubic used for part of the exp2 evaluations in prefix_tc.cu.
 
 2^x = 2^n * 2^f with n = round(x) and f = x - n in [-1/2, 1/2]; 2^f is
-approximated by c0 + c1 f + c2 f^2 + ...  The coefficients minimise the
+approximated by c0 + c1 f + c2 f^2 + c3 f^3.  The coefficients minimise the
 largest relative error over [-1/2, 1/2] (Lawson's iteratively reweighted
 least squares on a dense grid), then are rounded to fp32; the printed error
 is that of the fp32 coefficients.  A relative error of 7.5e-5 is far below
-half an ulp of bf16 (2^-9), the precision P is stored in; the quartic's 2.6e-6
-keeps the log-sum-exp as well.
+half an ulp of bf16 (2^-9), the precision P is stored in.
 
     python fit_exp2_poly.py
 """
@@ -31,8 +29,7 @@ def fit(degree=3, points=20001, iters=200):
 
 
 if __name__ == "__main__":
-    for degree in (3, 4):
-        c, e = fit(degree)
-        for i, v in enumerate(c):
-            print(f"c{i} = {float(v)!r}")
-        print(f"max relative error {e:.3g}")
+    c, e = fit()
+    for i, v in enumerate(c):
+        print(f"c{i} = {float(v)!r}")
+    print(f"max relative error {e:.3g}")
