@@ -97,11 +97,12 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
     return v;
 }
-__device__ __forceinline__ long long scan_add(long long v) {     // inclusive, over the warp
+template <typename T>
+__device__ __forceinline__ T scan_add(T v) {                     // inclusive, over the warp
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, v, k);
+        const T o = __shfl_up_sync(0xffffffffu, v, k);
         if (lane >= k) v += o;
     }
     return v;
@@ -144,9 +145,13 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
     if (warp == 0) {
         long long total = 0;
         for (int u = lane; u < units; u += 32) total += plan[u];
-        const long long work = warp_sum(total) * p.Hkv;
-        // (every CTA computes the same share; grid * share >= work)
-        const long long share = max(static_cast<long long>(static_cast<double>(work) / gridDim.x) + 1,
+        const long long work = (units == 1 ? plan[0] : warp_sum(total)) * p.Hkv;
+        // Work of less than 2^31 units is counted in 32 bits: a call of few keys
+        // has little else to do.  (Every CTA computes the same share; grid * share
+        // >= work.)
+        const bool small = work < (1LL << 31);
+        const long long share = max(small ? static_cast<long long>(static_cast<uint32_t>(work) / gridDim.x + 1)
+                                          : static_cast<long long>(static_cast<double>(work) / gridDim.x) + 1,
                                     static_cast<long long>(p.min_share));
         const long long begin = share * blockIdx.x, end = min(work, begin + share);
         Start st = {p.B, 0, 0, 0, 0, begin, end};
@@ -155,14 +160,15 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
             // `before`: the work before it
             long long before = 0;
             auto find = [&](long long c, int &k) {      // c: the lanes' costs (of all KV heads)
-                const long long cum = before + scan_add(c);
+                const long long cum = before + (small ? scan_add(static_cast<int>(c)) : scan_add(c));
                 const uint32_t past = __ballot_sync(0xffffffffu, cum > begin);
                 k = past ? __ffs(past) - 1 : 31;
                 before = __shfl_sync(0xffffffffu, past ? cum - c : cum, k);
                 return past != 0;
             };
             int k = 0, u = 0;
-            while (!find(u + lane < units ? plan[u + lane] * p.Hkv : 0, k) && u < units) u += 32;
+            if (units > 1)
+                while (!find(u + lane < units ? plan[u + lane] * p.Hkv : 0, k) && u < units) u += 32;
             u = min(u + k, units - 1);
             st.b = u;
             long long cost = plan[u];
@@ -174,14 +180,16 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
                 cost = __shfl_sync(0xffffffffu, c, k);
             }
             const Seq s = load_seq(p, st.b);
-            st.kvh = static_cast<int>(static_cast<double>(begin - before) / cost);
+            st.kvh = small ? static_cast<int>(static_cast<uint32_t>(begin - before) / static_cast<uint32_t>(cost))
+                           : static_cast<int>(static_cast<double>(begin - before) / cost);
             if ((st.kvh + 1) * cost <= begin - before) ++st.kvh;     // (the division's rounding)
             if (st.kvh * cost > begin - before) --st.kvh;
             before += cost * st.kvh;
-            // (bounded: lengths that another stream changed meanwhile must not hang the search)
-            while (!find(st.tile + lane < s.tiles ? item_cost(p, item_of(p, s, st.tile + lane)) : 0, k) &&
-                   st.tile < s.tiles)
-                st.tile += 32;
+            k = 0;
+            if (s.tiles > 1)        // (bounded: lengths that another stream changed meanwhile must not hang the search)
+                while (!find(st.tile + lane < s.tiles ? item_cost(p, item_of(p, s, st.tile + lane)) : 0, k) &&
+                       st.tile < s.tiles)
+                    st.tile += 32;
             st.tile += k;
             st.at = before;
         }
