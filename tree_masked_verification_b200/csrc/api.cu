@@ -131,12 +131,19 @@ float hta_api::scale_of(const longspec_hta_dims *d) {
     return d->scale > 0.f ? d->scale : 1.f / std::sqrt(static_cast<float>(d->D));
 }
 
-static int m_tiles_of(const longspec_hta_dims *d) {
+namespace {
+
+int m_tiles_of(const longspec_hta_dims *d) {
     const int M = (d->Hq / d->Hkv) * d->T;
     return (M + 127) / 128;
 }
 
-Chunking hta_api::chunking_for(const longspec_hta_dims *d, int requested, int num_sms) {
+// Split-KV chunking: chunk_tiles tiles of 128 keys per split, S splits.
+struct Chunking {
+    int S, chunk_tiles;
+};
+
+Chunking chunking_for(const longspec_hta_dims *d, int requested, int num_sms) {
     const int tiles = std::max(1, (d->L_cap + hta::kKeyTile - 1) / hta::kKeyTile);
     auto make = [&](int s) {
         s = std::max(1, std::min(std::min(s, tiles), hta::kMaxSplits));
@@ -158,7 +165,11 @@ Chunking hta_api::chunking_for(const longspec_hta_dims *d, int requested, int nu
     return best;
 }
 
-WsLayout hta_api::ws_layout(const longspec_hta_dims *d, int S) {
+struct WsLayout {
+    size_t o_off, lse_off, total;
+};
+
+WsLayout ws_layout(const longspec_hta_dims *d, int S) {
     const size_t rows = 1ull * d->B * d->Hq * d->T;
     WsLayout w;
     w.o_off = hta::kStatusBytes;
@@ -167,7 +178,7 @@ WsLayout hta_api::ws_layout(const longspec_hta_dims *d, int S) {
     return w;
 }
 
-static PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c, const void *q,
+PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c, const void *q,
                            const void *kp, const void *vp, const int32_t *plen, float *o_part,
                            float *lse_part, uint32_t *status) {
     PrefixParams p{};
@@ -188,7 +199,7 @@ static PrefixParams prefix_params(const longspec_hta_dims *d, const Chunking &c,
     return p;
 }
 
-static int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int kernel, cudaEvent_t ev_begin,
+int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int kernel, cudaEvent_t ev_begin,
                cudaEvent_t ev_end, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     const bool tc = kernel == LONGSPEC_HTA_PREFIX_TCGEN05;
@@ -210,7 +221,7 @@ static int run_prefix(const longspec_hta_dims *d, const PrefixParams &p, int ker
     return LONGSPEC_HTA_OK;
 }
 
-TreeMergeParams hta_api::tree_params(const longspec_hta_dims *d, int mode, int S, const void *q,
+TreeMergeParams tree_params(const longspec_hta_dims *d, int mode, int S, const void *q,
                             const void *kt, const void *vt, const int32_t *parent,
                             const int32_t *plen, const float *o_part, const float *lse_part,
                             uint32_t *status) {
@@ -229,6 +240,8 @@ TreeMergeParams hta_api::tree_params(const longspec_hta_dims *d, int mode, int S
     t.status = status;
     return t;
 }
+
+}  // namespace
 
 extern "C" {
 

@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include "../../include/longspec_hta.h"
-#include "hta_kernels.h"
 
 namespace hta_api {
 
@@ -30,20 +29,5 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int check_dims(const longspec_hta_dims *d);
 float scale_of(const longspec_hta_dims *d);
-
-// Split-KV chunking: chunk_tiles tiles of 128 keys per split, S splits.
-struct Chunking {
-    int S, chunk_tiles;
-};
-Chunking chunking_for(const longspec_hta_dims *d, int requested, int num_sms);
-
-struct WsLayout {
-    size_t o_off, lse_off, total;
-};
-WsLayout ws_layout(const longspec_hta_dims *d, int S);
-
-hta::TreeMergeParams tree_params(const longspec_hta_dims *d, int mode, int S, const void *q, const void *kt,
-                                 const void *vt, const int32_t *parent, const int32_t *plen, const float *o_part,
-                                 const float *lse_part, uint32_t *status);
 
 }  // namespace hta_api
