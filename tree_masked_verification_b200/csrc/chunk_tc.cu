@@ -378,33 +378,32 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     uint8_t *sv = smem + C::OFF_V + st * C::TILE;
                     const int a = w.it.lo - w.key0(j), z = w.it.hi - w.key0(j);   // live rows [a, z)
-                    // a row per lane, four rounds; all values in 16-byte pieces
+                    // A row per lane, four rounds, rounds of rows that every query row sees
+                    // left out (what such a row holds is everybody's).
                     for (int g = 0; g < 4; ++g) {
-                        const int r = g * 32 + lane;
+                        const int r = g * 32 + lane, key = w.key0(j) + r;
                         uint8_t *rp = sv + r * 128;
-                        uint32_t big = 0;
                         const bool live = r >= a && r < z;
-                        if (live) {
+                        const bool some = live && (key < w.it.all_lo || key >= w.it.all_hi);
+                        uint32_t word = 0;
+                        if (__any_sync(0xffffffffu, some || !live)) {
+                            uint32_t big = 0;           // bit 15 of a half: an exponent of all ones
+                            if (some) {
 #pragma unroll
-                            for (int h = 0; h < C::HALVES; ++h)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const uint4 u = *reinterpret_cast<const uint4 *>(rp + h * C::BOX + ((c ^ (r & 7)) << 4));
-                                    big = __vmaxu2(big, u.x & 0x7fff7fffu);
-                                    big = __vmaxu2(big, u.y & 0x7fff7fffu);
-                                    big = __vmaxu2(big, u.z & 0x7fff7fffu);
-                                    big = __vmaxu2(big, u.w & 0x7fff7fffu);
+                                for (int c = 0; c < C::HALVES * 8; ++c) {
+                                    const uint4 u = *reinterpret_cast<const uint4 *>(rp + (c >> 3) * C::BOX + (((c & 7) ^ (r & 7)) << 4));
+                                    big |= ((u.x & 0x7fff7fffu) + 0x00800080u) | ((u.y & 0x7fff7fffu) + 0x00800080u) |
+                                           ((u.z & 0x7fff7fffu) + 0x00800080u) | ((u.w & 0x7fff7fffu) + 0x00800080u);
                                 }
-                        }
-                        const bool inf = max(big & 0xffffu, big >> 16) >= 0x7f80u;
-                        if (!live || inf) {
+                            }
+                            const bool inf = (big & 0x80008000u) != 0;
+                            if (!live || inf) {
 #pragma unroll
-                            for (int h = 0; h < C::HALVES; ++h)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4 *>(rp + h * C::BOX + ((c ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                                for (int c = 0; c < C::HALVES * 8; ++c)
+                                    *reinterpret_cast<uint4 *>(rp + (c >> 3) * C::BOX + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            word = __ballot_sync(0xffffffffu, inf);
                         }
-                        const uint32_t word = __ballot_sync(0xffffffffu, inf);
                         if (lane == 0) s_poison[(pos % kPoisonRing) * 4 + g] = word;
                     }
                     fence_proxy_async();
