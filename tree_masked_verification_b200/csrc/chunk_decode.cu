@@ -54,7 +54,8 @@ struct DecCfg {
     static constexpr int OFF_STAT = OFF_JOIN + kDecWarps * ROWS * ROW * 4;   // [warp][row][m, l, M, bad]
     static constexpr int OFF_BAR = OFF_STAT + kDecWarps * ROWS * 16;
     static constexpr int OFF_MISC = OFF_BAR + 2 * NS * 8;   // abort; Start
-    static constexpr int SMEM = OFF_MISC + 64;
+    static constexpr int SMEM = OFF_MISC + 16 + 80;
+    static_assert(sizeof(Start) <= 80, "room of the plan's result");
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(kPlanUnits * 8 <= OFF_SCALE, "the plan's scratch lies in the stages");
@@ -118,7 +119,6 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && warp == 0) check_ranges(p.q_start, p.B, p.N, p.status);
     plan_start(p, reinterpret_cast<long long *>(smem + C::OFF_STAGE), s_start);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");     // the plan's scratch becomes a stage
     __syncthreads();
@@ -170,6 +170,7 @@ chunk_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (++st == C::NS) { st = 0; ph ^= 1; }
             }
         }
+        if (blockIdx.x == 0) check_ranges(p.q_start, p.B, p.N, p.status);
         __syncwarp();
         if (lane == 0 && *s_abort)                      // let the copies in flight land
             for (int i = max(0, issued - C::NS); i < issued; ++i) mbar_wait(full + i % C::NS, (i / C::NS) & 1);

@@ -118,6 +118,7 @@ __device__ __forceinline__ long long seq_cost(const ChunkParams &p, const Seq &s
 struct Start {
     int b, kvh, tile, pad;
     long long at, begin, end;       // units: start of that item, this CTA's range
+    Seq s;                          // sequence b
 };
 
 // The share of the work of each CTA, and where this CTA's begins (the whole
@@ -154,7 +155,7 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
                                           : static_cast<long long>(static_cast<double>(work) / gridDim.x) + 1,
                                     static_cast<long long>(p.min_share));
         const long long begin = share * blockIdx.x, end = min(work, begin + share);
-        Start st = {p.B, 0, 0, 0, 0, begin, end};
+        Start st = {p.B, 0, 0, 0, 0, begin, end, {}};
         if (begin < work) {
             // the unit of sequences, the sequence, the KV head and the item that hold `begin`;
             // `before`: the work before it
@@ -191,6 +192,7 @@ static __device__ void plan_start(const ChunkParams &p, long long *plan, Start *
                        st.tile < s.tiles)
                     st.tile += 32;
             st.tile += k;
+            st.s = s;
             st.at = before;
         }
         if (lane == 0) *out = st;
@@ -214,7 +216,7 @@ struct Walk {
         at = st->at;
         begin = st->begin;
         end = st->end;
-        if (b < p.B) s = load_seq(p, b);
+        s = st->s;
     }
     __device__ __forceinline__ bool next(const ChunkParams &p) {
         for (;;) {

@@ -97,7 +97,8 @@ struct Cfg {
     static_assert(kPoisonRing >= NK + 2, "see kPoisonRing");
     static constexpr int OFF_POISON = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // [kPoisonRing][4] words
     static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort; Start
-    static constexpr int OFF_PARENT = OFF_MISC + 64;                 // parent + 1 of each node, a byte (trees)
+    static_assert(sizeof(Start) <= 80, "room of the plan's result");
+    static constexpr int OFF_PARENT = OFF_MISC + 96;                 // parent + 1 of each node, a byte (trees)
     static constexpr int OFF_SCALE = OFF_PARENT + kTMax;             // per K stage: scale bytes of K and of V; per V stage: V's
     static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 + NV * 128 : 0);   // walks: softmax groups, K and V loaders
     static constexpr int WALK_BYTES = 128;
@@ -273,7 +274,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     // lengths, queries and the cache may come from the previous kernel
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!p.tree && blockIdx.x == 0 && warp == 0) check_ranges(p.q_start, p.B, p.N, p.status);
     plan_start(p, reinterpret_cast<long long *>(smem + C::OFF_PLAN), s_start);
     fence_proxy_async();                            // the plan's scratch becomes the K ring
     tc_fence_before();
@@ -412,6 +412,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
             }
         }
+        if (!p.tree && blockIdx.x == 0) check_ranges(p.q_start, p.B, p.N, p.status);
         __syncwarp();
     } else if (warp == kWarpMma) {
         // -------------------------------------------------------------- MMA
@@ -657,29 +658,38 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             float c2_row = p.scale_log2;
             // ---- Q into shared memory (one row tile: each group half of the columns)
             {
+                // The warp's 32 rows, a row's pieces on neighbouring lanes: a load per row
+                // and thread touched 32 lines each time, 4 us an item.
                 const int ch0 = two ? 0 : grp * (D / 16), nch = two ? D / 8 : D / 16;
-                uint4 qv[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    if (Q8 || i < nch)
-                        qv[i] = valid ? reinterpret_cast<const uint4 *>(qp)[Q8 ? i : ch0 + i] : make_uint4(0u, 0u, 0u, 0u);
-                float mul = 1.f;
-                if constexpr (Q8) {                     // (the shift takes the whole row's largest value)
-                    uint32_t big = 0;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) big = max_bits(qv[i], big);
-                    const int up = f16_shift(halves_max(big), 100);
-                    mul = pow2(up);
-                    c2_row = p.scale_log2 * pow2(-up);
-                }
+                const int cs = Q8 || two ? (D == 128 ? 4 : 3) : (D == 128 ? 3 : 2);   // log2 of the pieces read of a row
+                const int rpi = 32 >> cs, ch = (Q8 ? 0 : ch0) + (lane & ((1 << cs) - 1));
+                const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+                const unsigned long long q_at = reinterpret_cast<unsigned long long>(qp);
                 if (ok) ok = warp_wait(q_empty, items + 1);
-                uint8_t *qs = smem + C::OFF_Q + (two ? grp * C::TILE : 0) + r * 128;
+                uint8_t *qs = smem + C::OFF_Q + (two ? grp * C::TILE : 0) + wq * 32 * 128;
+                for (int i0 = 0; i0 < (1 << cs); i0 += 4) {
+                    uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const int ch = Q8 ? i : ch0 + i;
-                    if (Q8 ? i >= ch0 && i < ch0 + nch : i < nch)
-                        *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::BOX + (((ch & 7) ^ (r & 7)) << 4)) =
-                            Q8 ? to_f16(qv[i], mul) : qv[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = (i0 + i) * rpi + (lane >> cs);
+                        const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, q_at, rr));
+                        v[i] = (rows >> rr) & 1u ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = (i0 + i) * rpi + (lane >> cs);
+                        uint4 y = v[i];
+                        if constexpr (Q8) {             // (the shift takes the whole row's largest value)
+                            uint32_t big = halves_max(max_bits(v[i], 0u));
+                            for (int o = 1; o < (1 << cs); o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            const int up = f16_shift(big, 100);
+                            const int mine = __shfl_sync(0xffffffffu, up, (lane & (rpi - 1)) << cs);
+                            if (lane / rpi == i0 + i) c2_row = p.scale_log2 * pow2(-mine);
+                            y = to_f16(v[i], pow2(up));
+                        }
+                        if (ch >= ch0 && ch < ch0 + nch)
+                            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::BOX + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = y;
+                    }
                 }
                 fence_proxy_async();
                 __syncwarp();
