@@ -47,13 +47,13 @@
 // holds bf16's 8 bits down to 2^-28 of the row's largest value.
 //
 // Measured (B200, 1965 MHz, at the power cap in long runs): prefill of 4096
-// tokens behind 12288, 32 heads over 8: 0.95 ms, 1.0 PFLOP/s, 0.62 of cuBLAS's
+// tokens behind 12288, 32 heads over 8: 0.92 ms, 1.05 PFLOP/s, 0.65 of cuBLAS's
 // rate.  A pair of 128 x 128 tiles takes 3.7 k cycles against 2048 of MMA: the
 // chain of a group is its softmax (1.9 k), the MMAs of the next scores behind it
 // (1.0 k) and hand-overs, and two groups fill the MMAs to 55-60 %; issuing eight
 // MMAs takes 70 cycles, and no pipe is above 45 %.  Decode of 16 sequences, bf16:
-// 205-215 us, 0.88-0.93 of the measured copy.  A 68-node tree over e4m3 keys,
-// 8 x 32 heads: 307 us, 2.6 TB/s of codes: 3.0 k cycles a 128-key tile, of which
+// 205-211 us, 0.90-0.93 of the measured copy.  A 68-node tree over e4m3 keys,
+// 8 x 32 heads: 301-310 us, 2.6 TB/s of codes: 3.0 k cycles a 128-key tile, of which
 // the conversion's traffic in shared memory beside the MMAs' own costs 0.6 k
 // (without it 2.4 k).
 //
@@ -205,6 +205,8 @@ __device__ __forceinline__ uint4 to_f16(uint4 u, float mul) {
 __device__ __forceinline__ int f16_shift(uint32_t big, int most) {
     return max(min(14 - (static_cast<int>(big >> 7) - 127), most), -100);
 }
+
+template <int N> struct Int { static constexpr int value = N; };
 
 constexpr int kLeastE = 96;         // least scale of a tile
 
@@ -917,6 +919,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 l = a0 * l0 + a1 * l1;
                 row_nan = l0 != l0 || l1 != l1;
                 has1 = n_tiles > 1;
+                if constexpr (!Q8) bar_sync(1, 256);    // (rows are staged there next)
             } else if (!ok) {
                 row_nan = true;
             }
@@ -928,33 +931,71 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const long long prow = slot_row(p, blockIdx.x, which) + row;
             const int col0 = two ? 0 : grp * (D / 2), col1 = two ? D : col0 + D / 2;
             if (warp_active) {
+                // W columns at a time.  bf16 caches: the rows leave by way of shared memory
+                // (Q's, which has been read), so that a store covers whole pieces of few rows
+                // (two chunks of 500 tokens 41.6 -> 37.9 us against a row per thread); the
+                // trees over e4m3 caches lose 2-3 % by it and store a row per thread.
+                constexpr int W = Q8 || C::OFF_K >= 32768 ? 32 : 16;
+                static_assert(Q8 || 8 * 32 * W * 4 <= C::OFF_K, "a piece of W columns per warp");
                 const float f0 = a0 * inv * o0, f1 = a1 * inv * o1;
                 const uint32_t to0 = t_o + (two ? grp * D : 0), to1 = t_o + D;
+                uint8_t *buf = smem + C::OFF_Q + (warp - kWarpSoftmax) * 32 * W * 4;
+                const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+                const int my_row = whole ? static_cast<int>(orow) : row;    // (2^31 rows of out would be 256 GB)
+                // the Q 16-byte pieces of each lane's row, piece(i) the i-th: to dst + row * row_bytes
+                auto store = [&](auto pieces, auto piece, uint8_t *dst, int row_bytes) {
+                    constexpr int Q = decltype(pieces)::value;
+                    if constexpr (Q8) {
+                        if (valid) {
+#pragma unroll
+                            for (int i = 0; i < Q; ++i)
+                                *reinterpret_cast<uint4 *>(dst + static_cast<long long>(my_row) * row_bytes + i * 16) = piece(i);
+                        }
+                        __syncwarp();
+                    } else {
+                        // piece i of a row at i XOR the row's place among those that share 128 bytes
+                        auto at = [&](int rr, int i) { return reinterpret_cast<uint4 *>(buf) + rr * Q + (i ^ (rr * Q / 8 & (Q - 1))); };
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) *at(lane, i) = piece(i);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            const int rr = (i * 32 + lane) / Q, q = lane % Q;
+                            const long long to = __shfl_sync(0xffffffffu, my_row, rr);
+                            const uint4 v = *at(rr, q);
+                            if ((rows >> rr) & 1u) *reinterpret_cast<uint4 *>(dst + to * row_bytes + q * 16) = v;
+                        }
+                        __syncwarp();
+                    }
+                };
 #pragma unroll 1
-                for (int col = col0; col < col1; col += 32) {
-                    uint32_t x0[32], x1[32];
-                    float y[32];
-                    tmem_ld32(to0 + col, x0);
-                    if (has1) tmem_ld32(to1 + col, x1);
+                for (int col = col0; col < col1; col += W) {
+                    uint32_t x0[W], x1[W];
+                    float y[W];
+                    if constexpr (W == 32) {
+                        tmem_ld32(to0 + col, x0);
+                        if (has1) tmem_ld32(to1 + col, x1);
+                    } else {
+                        tmem_ld16(to0 + col, x0);
+                        if (has1) tmem_ld16(to1 + col, x1);
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < W; ++i) {
                         y[i] = __uint_as_float(x0[i]) * f0;
                         if (has1) y[i] = fmaf(__uint_as_float(x1[i]), f1, y[i]);
                         if (l == 0.f && !row_nan) y[i] = 0.f;
                     }
-                    if (valid && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                                pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
-                    } else if (valid) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.o_part + prow * D + col);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                    }
-                    __syncwarp();
+                    if (whole)
+                        store(Int<W / 8>(), [&](int i) {
+                            return make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                              pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+                        }, reinterpret_cast<uint8_t *>(p.out) + col * 2, D * 2);
+                    else
+                        store(Int<W / 4>(), [&](int i) {
+                            return make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                              __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+                        }, reinterpret_cast<uint8_t *>(p.o_part + slot_row(p, blockIdx.x, which) * D + col), D * 4);
                 }
                 if (valid && (two || grp == 0)) {
                     if (whole) p.lse[orow] = lse;
