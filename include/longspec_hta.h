@@ -545,8 +545,10 @@ LONGSPEC_HTA_API int longspec_hta_chunk_attention_paged(const longspec_hta_dims 
 /* longspec_hta_verify_paged, longspec_hta_prefix_attention_paged and
  * longspec_hta_commit_paged over a cache held in e4m3 (both scales set; a
  * bf16 cache is INVALID_OPTION here).  k_tree and v_tree stay bf16; the
- * commit stores the accepted rows in e4m3.  Arguments, results and errors
- * otherwise as those calls; the attention calls' workspace is
+ * commit stores the accepted rows in e4m3.  The products run on f16: rows of
+ * q, k_tree and v_tree are scaled into its range by powers of two, where
+ * values less than 2^-28 of their row's largest lose bits.  Arguments,
+ * results and errors otherwise as those calls; the attention calls' workspace is
  * longspec_hta_q8_workspace_bytes(dims). */
 LONGSPEC_HTA_API size_t longspec_hta_q8_workspace_bytes(const longspec_hta_dims *dims);
 LONGSPEC_HTA_API int longspec_hta_verify_paged_q8(const longspec_hta_dims *dims, const void *q,

@@ -38,13 +38,18 @@
 // registers, one tile ahead, took 5 us a tile: a warp's waits on them cover
 // younger loads too, so that each tile waited for the next one's.)  The MMAs
 // run in f16: every code is one of f16's numbers, and two conversions and two
-// products make four of them where bf16 takes ten instructions.  A tile's
-// rows are scaled to its largest scale E (rows 2^-24 below it vanish beside
-// it); 2^(E - 127) goes to the scores, or for V to the weights, against a
-// running reference e_run by which the output is multiplied at the end.  E is
-// at least 96 (values of 2e-7): an all-zero tile must not drive the weights
-// out of fp32's range.  Query rows are scaled by powers of two into f16, which
-// holds bf16's 8 bits down to 2^-28 of the row's largest value.
+// products make four of them where bf16 takes ten instructions.  A tile's rows
+// are brought to its largest scale E where none lies more than 15 octaves below
+// it (K; no code leaves f16's numbers) or 4 (V), and 2^(E - 127) goes to the
+// scores, or for V to the weights.  Tiles of rows further apart keep the codes
+// as they are, and each key's scale byte goes to its own score or weight (8
+// trees with every tile such: 571 us against 287).  The weights P stand relative
+// to the running maximum of x + scale of V, kept as m_run + e_run, so that they
+// stay in f16's range beside tiles of large values or of zeros; from E alone the
+// maximum comes out 4 octaves too high at most, which is why V's limit is low.
+// Rows of queries and of the tree are scaled by powers of two into f16 (the
+// tree's by the tile or by the row, as above), which holds bf16's 8 bits down to
+// 2^-28 of the row's largest value.
 //
 // Measured (B200, 1965 MHz, at the power cap in long runs): prefill of 4096
 // tokens behind 12288, 32 heads over 8: 0.92 ms, 1.05 PFLOP/s, 0.65 of cuBLAS's
@@ -58,7 +63,7 @@
 // (without it 2.4 k).
 //
 // Tensor memory: S[g] columns 128g.. (fp32 scores; P as 16-bit pairs over its
-// first 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
+// last 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
 // for the tensor cores, relative 2^-9 on average, the same size as the output's
 // own rounding; its sum l, the maximum and O stay in fp32.  The running maximum
 // moves only when it grew by more than 2^8 (exact after the division by l).
@@ -74,7 +79,7 @@ namespace hta {
 
 namespace {
 
-// NaN words of the tiles in flight: K of tile p is there at the earliest when
+// NaN words and scale bytes of the tiles in flight: K of tile p is there at the earliest when
 // the softmax of tile p - NK - 2 is done, so NK + 2 places are enough
 constexpr int kPoisonRing = 6;
 
@@ -99,8 +104,9 @@ struct Cfg {
     static constexpr int OFF_MISC = OFF_POISON + kPoisonRing * 16;   // tmem base, abort; Start
     static_assert(sizeof(Start) <= 80, "room of the plan's result");
     static constexpr int OFF_PARENT = OFF_MISC + 96;                 // parent + 1 of each node, a byte (trees)
-    static constexpr int OFF_SCALE = OFF_PARENT + kTMax;             // per K stage: scale bytes of K and of V; per V stage: V's
-    static constexpr int OFF_WALK = OFF_SCALE + (Q8 ? NK * 256 + NV * 128 : 0);   // walks: softmax groups, K and V loaders
+    static constexpr int OFF_SCALE = OFF_PARENT + kTMax;             // per tile in flight: scale bytes of K and of V
+    static constexpr int OFF_SCALE_V = OFF_SCALE + (Q8 ? kPoisonRing * 256 : 0);   // per V stage: V's once more, for the V loaders
+    static constexpr int OFF_WALK = OFF_SCALE_V + (Q8 ? NV * 128 : 0);     // walks: softmax groups, K and V loaders
     static constexpr int WALK_BYTES = 128;
     static constexpr int OFF_EXP = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;   // per tile in flight: E of K, E of V
     static constexpr int OFF_RED = OFF_EXP + (Q8 ? kPoisonRing * 8 : 0);   // [2][4] words: a maximum over a loader set
@@ -201,14 +207,17 @@ __device__ __forceinline__ uint4 to_f16(uint4 u, float mul) {
     return make_uint4(pack_f16x2(bf16_lo(u.x) * mul, bf16_hi(u.x) * mul), pack_f16x2(bf16_lo(u.y) * mul, bf16_hi(u.y) * mul),
                       pack_f16x2(bf16_lo(u.z) * mul, bf16_hi(u.z) * mul), pack_f16x2(bf16_lo(u.w) * mul, bf16_hi(u.w) * mul));
 }
-// the shift that brings a largest bit pattern into [2^14, 2^15), within [-100, most]
+// the shift that brings a largest bit pattern into [2^14, 2^15), at most `most`
 __device__ __forceinline__ int f16_shift(uint32_t big, int most) {
-    return max(min(14 - (static_cast<int>(big >> 7) - 127), most), -100);
+    return max(min(14 - (static_cast<int>(big >> 7) - 127), most), -113);
 }
 
 template <int N> struct Int { static constexpr int value = N; };
 
-constexpr int kLeastE = 96;         // least scale of a tile
+// Octaves between a tile's largest and least row scale up to which its rows are
+// brought to the largest (see the head of this file)
+constexpr int kSpreadK = 15, kSpreadV = 4;
+constexpr int kEach = 256;          // bit of a tile's scale: its rows keep their own
 
 // registers of a tensor-memory load that has been waited for
 __device__ __forceinline__ void pin(uint32_t (&r)[32]) {
@@ -340,11 +349,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         if constexpr (Q8) {
                             tma_load_2d(stage + C::TILE - C::RAW + (lane << bsh) * D, map, full + st, 0, y);
                             if (is_k) {                 // (V's scale bytes too: see the K loaders)
-                                uint8_t *sc = s_scale + st * 256 + (lane << bsh);
+                                uint8_t *sc = s_scale + issued % kPoisonRing * 256 + (lane << bsh);
                                 bulk_load(sc, p.cache.k_scale + y, bs, full + st);
                                 bulk_load(sc + 128, p.cache.v_scale + y, bs, full + st);
                             } else {
-                                bulk_load(s_scale + C::NK * 256 + st * 128 + (lane << bsh), p.cache.v_scale + y, bs, full + st);
+                                bulk_load(smem + C::OFF_SCALE_V + st * 128 + (lane << bsh), p.cache.v_scale + y, bs, full + st);
                             }
                         } else {
 #pragma unroll
@@ -538,17 +547,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         make_uint4(a.x, a.y, b.x, b.y);
                 }
             };
-            // largest scale byte of the live rows [a, z) (NaN rows aside), at least
-            // kLeastE; w4: bytes of rows 4 * lane ..
-            auto tile_exp = [&](uint32_t w4, int a, int z) {
-                int e = kLeastE;
+            // largest scale byte of the live rows [a, z) (NaN rows aside), with kEach where
+            // the least lies more than `spread` below it; w4: bytes of rows 4 * lane ..
+            auto tile_exp = [&](uint32_t w4, int a, int z, int spread) {
+                uint32_t most = kScaleMin, least = kScaleNan;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int x = (w4 >> (8 * i)) & 255, r = 4 * lane + i;
-                    if (r >= a && r < z && x != kScaleNan) e = max(e, x);
+                    const uint32_t x = (w4 >> (8 * i)) & 255, r = 4 * lane + i;
+                    if (static_cast<int>(r) >= a && static_cast<int>(r) < z && x != kScaleNan) {
+                        most = max(most, x);
+                        least = min(least, x);
+                    }
                 }
-                return min(static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(e))), kScaleMax);
+                most = __reduce_max_sync(0xffffffffu, most);
+                least = __reduce_min_sync(0xffffffffu, least);
+                return static_cast<int>(most) | (most > least + spread ? kEach : 0);
             };
+            const int spread = is_v ? kSpreadV : kSpreadK;
             for (;;) {
                 bar_sync(set_bar, 128);
                 if (first_thread) *more = lwk.next(p);
@@ -564,24 +579,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     if (j < cache_tiles) {
                         const int a = lo - (base + j * 128), z = hi - (base + j * 128);
                         const bool live = row >= a && row < z;
-                        const uint8_t *sc = is_v ? s_scale + C::NK * 256 + st * 128 : s_scale + st * 256;
+                        const uint8_t *sc = is_v ? smem + C::OFF_SCALE_V + st * 128 : s_scale + at * 256;
                         const uint8_t *scv = is_v ? sc : sc + 128;
                         const int e = sc[row], ev = scv[row];
-                        const uint32_t e4 = *reinterpret_cast<const uint32_t *>(sc + 4 * lane);
-                        const int E = tile_exp(e4, a, z);
+                        const int E = tile_exp(*reinterpret_cast<const uint32_t *>(sc + 4 * lane), a, z, spread);
                         if (!is_v) {
                             // V rows held as NaN, and V's E, are told to the softmax groups with K
                             const uint32_t nan = __ballot_sync(0xffffffffu, live && ev == kScaleNan);
-                            const int Ev = tile_exp(*reinterpret_cast<const uint32_t *>(scv + 4 * lane), a, z);
+                            const int Ev = tile_exp(*reinterpret_cast<const uint32_t *>(scv + 4 * lane), a, z, kSpreadV);
                             if (lane == 0) *word = nan;
                             if (first_thread) s_exp[at] = make_int2(E, Ev);
                         }
                         read_row(stage);
-                        write_row(stage, !live ? 0u : e != kScaleNan ? f16_pow2(min(e - E, 0)) : is_v ? 0u : 0x7e007e00u);
+                        write_row(stage, !live ? 0u : e != kScaleNan ? f16_pow2(E & kEach ? 0 : e - E) : is_v ? 0u : 0x7e007e00u);
                     } else {
-                        // tree rows (bf16), one a lane, scaled into f16 by the tile's largest value.
-                        // Rows behind the tree are zeroed, and so are V rows with an infinity or a
-                        // NaN, which are told to the softmax groups (they wait for this tile).
+                        // tree rows (bf16), one a lane, scaled into f16 by the tile's largest value or,
+                        // where the rows' largest values lie far apart, by their own (2^(127 - e);
+                        // rows of zeros are zeros under any).  Rows behind the tree are zeroed, and so
+                        // are V rows with an infinity or a NaN, which are told to the softmax groups
+                        // (they wait for this tile).
                         const int r = lw * 32 + lane, live = min(128, p.N - (j - cache_tiles) * 128);
                         uint8_t *rp = stage + r * 128;
                         auto piece = [&](int x) { return reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)); };
@@ -591,18 +607,29 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         big = halves_max(big);
                         const bool inf = big >= 0x7f80u, zero = r >= live || (is_v && inf);
                         uint32_t *red = reinterpret_cast<uint32_t *>(smem + C::OFF_RED) + (is_v ? 4 : 0);
-                        const uint32_t wm = __reduce_max_sync(0xffffffffu, r < live && !inf ? big : 0u);
+                        const int e = 127 - f16_shift(big, 112);        // 15 .. 240
+                        const bool counts = r < live && !inf && big != 0;
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, counts ? e : 15);
+                        const uint32_t least = __reduce_min_sync(0xffffffffu, counts ? e : 255);
                         bar_sync(set_bar, 128);
-                        if (lane == 0) red[lw] = wm;
+                        if (lane == 0) red[lw] = most | (least << 16);
                         bar_sync(set_bar, 128);
-                        const int up = f16_shift(max(max(red[0], red[1]), max(red[2], red[3])), 127 - kLeastE);
+                        int E = 15, lowest = 255;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            E = max(E, static_cast<int>(red[i] & 0xffffu));
+                            lowest = min(lowest, static_cast<int>(red[i] >> 16));
+                        }
+                        const bool each = E > lowest + spread;
+                        const float mul = pow2(127 - (each ? e : E));
 #pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x) *piece(x) = zero ? make_uint4(0u, 0u, 0u, 0u) : to_f16(*piece(x), pow2(up));
+                        for (int x = 0; x < D / 8; ++x) *piece(x) = zero ? make_uint4(0u, 0u, 0u, 0u) : to_f16(*piece(x), mul);
+                        s_scale[at * 256 + (is_v ? 128 : 0) + r] = static_cast<uint8_t>(e);
                         if (is_v) {
                             const uint32_t nan = __ballot_sync(0xffffffffu, r < live && inf);
                             if (lane == 0) *word = nan;
                         }
-                        if (first_thread) (is_v ? s_exp[at].y : s_exp[at].x) = 127 - up;
+                        if (first_thread) (is_v ? s_exp[at].y : s_exp[at].x) = E | (each ? kEach : 0);
                     }
                     fence_proxy_async();
                     __syncwarp();
@@ -716,7 +743,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
             const int it_base = w.it.base, it_all_lo = w.it.all_lo, it_all_hi = w.it.all_hi, it_cache_tiles = w.it.cache_tiles;
             float m_run = -INFINITY;
-            int e_run = 0;                                  // (e4m3) scale of O: 2^(e_run - 127)
+            float e_run = 0.f;                              // (e4m3) O is in units of 2^(m_run + e_run - 127)
             uint64_t l2 = 0;
             const int j0 = w.j0, n_tiles = w.j1 - j0;
             const int step = two ? 1 : 2;
@@ -762,19 +789,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     float c2 = c2_row;
                     bool resc = false;
                     float alpha = 1.f, shift = 0.f;         // P is 2^(x - m + shift)
-                    if constexpr (Q8) {
-                        const int2 E = s_exp[(pos + jj) % kPoisonRing];
-                        c2 *= pow2(E.x - 127);
-                        // f16 holds 2^8 (the stale maximum) times 2^7: only a larger step moves e_run
-                        if (jj < step) {
-                            e_run = E.y;
-                        } else if (E.y > e_run + 7) {
-                            alpha = ex2(static_cast<float>(e_run - E.y));
-                            resc = true;
-                            e_run = E.y;
-                        }
-                        shift = static_cast<float>(E.y - e_run);
-                    }
                     // Passes over the row's 128 scores, 32 at a time, from tensor memory each
                     // time: hidden keys to -inf (partly visible tiles), the maximum, the
                     // weights.  One pass with all 128 in registers took the same time (983
@@ -791,6 +805,45 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             tmem_st32(t_s + 32 * q, x);
                         }
                         tmem_wait_st();
+                    }
+                    // (e4m3) the scales of the tile's rows, or the codes as they are and each
+                    // row's own scale: K's on the scores, V's on the weights
+                    bool each_v = false;
+                    float e_v = 0.f, top = -INFINITY;       // V's scale; with each_v the largest x + scale
+                    const uint8_t *keys = s_scale + ((pos + jj) % kPoisonRing) * 256;
+                    if constexpr (Q8) {
+                        const int2 E = s_exp[(pos + jj) % kPoisonRing];
+                        const bool each_k = (E.x & kEach) != 0;
+                        each_v = (E.y & kEach) != 0;
+                        e_v = static_cast<float>(E.y & 255);
+                        if (each_k || each_v) {
+                            if (!each_k) c2 *= pow2((E.x & 255) - 127);
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t x[16];
+                                tmem_ld16(t_s + 16 * q, x);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float y = __uint_as_float(x[i]);
+                                    if (each_k) {           // (a hidden key's byte may be anything)
+                                        const float k = c2 * __uint_as_float(static_cast<uint32_t>(keys[16 * q + i]) << 23);
+                                        y = y == -INFINITY ? y : y * k;
+                                        x[i] = __float_as_uint(y);
+                                    } else {
+                                        y *= c2;
+                                    }
+                                    top = fmaxf(top, y + static_cast<float>(keys[128 + 16 * q + i]));
+                                }
+                                if (each_k) tmem_st16(t_s + 16 * q, x);
+                            }
+                            if (each_k) {
+                                tmem_wait_st();
+                                c2 = 1.f;
+                            }
+                        } else {
+                            c2 *= pow2(E.x - 127);
+                        }
                     }
                     float mt = -INFINITY;
                     uint32_t x[2][32];                  // two quarters, the next on its way
@@ -810,13 +863,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     const float m_tile = mt * c2;
                     if (m_tile != m_tile) row_nan = true;
+                    if (!each_v) top = m_tile + e_v;
                     if (m_tile > m_run + 8.f) {
-                        const float a = ex2(m_run - m_tile);   // 0 on the first tile with a visible key
+                        const float d = m_run - m_tile, a = ex2(d);   // 0 on the first tile with a visible key
                         l2 = fma2(l2, f2(a, a), 0ull);
-                        alpha *= a;
+                        alpha = a;
                         resc = jj >= step;                  // (O holds nothing before the group's second tile)
                         m_run = m_tile;
+                        if constexpr (Q8) {                 // the reference m_run + e_run stays or grows
+                            const float e = fmaxf(rintf(d + e_run), ceilf(top - m_run));
+                            alpha = ex2(d + (e_run - e));
+                            e_run = e;
+                        }
+                    } else if (Q8 && top > m_run + e_run + 8.f) {
+                        const float e = ceilf(top - m_run);
+                        alpha = ex2(e_run - e);
+                        resc = jj >= step;
+                        e_run = e;
                     }
+                    if constexpr (Q8) shift = each_v ? 0.f : fmaxf(e_v - e_run, -60.f);   // (2^-52 is 0 in f16)
                     if (__any_sync(0xffffffffu, resc)) {
                         // this tile's scores were committed after P*V of the group's previous
                         // tile, so O[grp] is complete, and P*V of this tile waits for this warp
@@ -869,7 +934,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         pin(x[0]);
                         weights(x[1], 1);
                         weights(x[0], 0);
-                    } else {                            // (as a loop: fewer registers)
+                    } else if (!each_v) {               // (as a loop: fewer registers)
 #pragma unroll 1
                         for (int q = 3; q >= 0; --q) {
                             uint32_t y[32];
@@ -877,6 +942,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             tmem_wait_ld();
                             pin(y);
                             weights(y, q);
+                            if (q == 2) half_done();
+                        }
+                    } else {
+                        // (w 2^(127 - e_run)) 2^(e - 127): neither leaves fp32's range upwards, e and
+                        // e_run being 15 at least; what underflows is 0 in f16.  (255, a NaN row or
+                        // one nobody sees: a number for the weight of 0 to meet.)
+                        const float unit = ex2(127.f - e_run);
+                        const uint64_t uu = f2(unit, unit);
+#pragma unroll 1
+                        for (int q = 3; q >= 0; --q) {
+                            uint32_t y[32];
+                            tmem_ld32(t_s + 32 * q, y);
+                            tmem_wait_ld();
+                            const uint8_t *e = keys + 128 + 32 * q;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 z = unf2(fma2(f2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), cc, nm));
+                                const uint64_t w = f2(ex2(z.x), ex2(z.y));
+                                lt = add2(lt, w);
+                                const float2 u = unf2(fma2(w, uu, 0ull));
+                                y[k] = pack_f16x2(u.x * __uint_as_float(min(static_cast<uint32_t>(e[2 * k]), 254u) << 23),
+                                                  u.y * __uint_as_float(min(static_cast<uint32_t>(e[2 * k + 1]), 254u) << 23));
+                            }
+                            tmem_st16(t_s + 64 + 16 * q, y);
                             if (q == 2) half_done();
                         }
                     }
@@ -901,7 +990,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float2 lp = unf2(l2);
             float l = m_run == -INFINITY ? 0.f : lp.x + lp.y, m = m_run;
             float a0 = 1.f, a1 = 0.f;
-            float o0 = Q8 ? pow2(e_run - 127) : 1.f, o1 = 1.f;      // scales of O[0], O[1] (two row tiles: of the own)
+            float o0 = Q8 ? ex2(e_run - 127.f) : 1.f, o1 = 1.f;      // scales of O[0], O[1] (two row tiles: of the own)
             bool has1 = false;
             if (!two) {                                     // join the groups: key tiles 0, 2, .. and 1, 3, ..
                 float *xch = reinterpret_cast<float *>(smem + C::OFF_XCH);
