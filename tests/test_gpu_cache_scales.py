@@ -182,3 +182,101 @@ def test_a_nan_row_beside_scales_far_apart(new, Hq, window):
                 assert torch.equal(out[t], good[t]), t
         cache.copy_(keep[0])
         scale.copy_(keep[1])
+
+
+# -------------------------------------------- several tiles of an item in one CTA
+MANY = [(2, 16), (30, 16), (40, 16)]            # few rows; one row tile; two (4 KV heads)
+
+
+def many(new, Hq, D, seed):
+    """Enough sequences that a CTA takes whole items: references carried from
+    tile to tile, not joined from partials.  And the rows to look at."""
+    c = Case([700] * 60, [new] * 60, Hq, 4, D, 32, True, seed=seed)
+    rows = {(b * new + t, h) for b in (0, 7, 30, 59) for t in {0, new // 2, new - 1} for h in (0, Hq // 2, Hq - 1)}
+    return c, rows
+
+
+@pytest.mark.parametrize("k", [6, 14, 20, 26, 60])
+@pytest.mark.parametrize("new,Hq", MANY)
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_of_hardly_any_weight_many(new, Hq, D, k):
+    c, rows = many(new, Hq, D, k + new)
+    c.vs.copy_(torch.where(c.vs != 255, 70, c.vs.int()).to(torch.uint8))
+    first = c.table[:, 0].long()
+    c.vs[first, :, 3:9] = 70 + k
+    c.check(window=600, rows=rows)
+    u = randn(D, seed=1).float()
+    c.q = (c.q.float() * 0.5 + u).to(torch.bfloat16)
+    codes, e = Case.quantise((-u * 24).to(torch.bfloat16)[None])
+    for at in range(3, 9):
+        c.kc[first, :, at], c.ks[first, :, at] = codes[0], e[0]
+    c.check(rows=rows)
+    third = c.table[:, 9].long()                        # the same, met last
+    c.vs[first, :, 3:9] = 70
+    c.vs[third, :, 5] = 70 + k
+    c.kc[third, :, 5], c.ks[third, :, 5] = codes[0], e[0]
+    c.check(rows=rows)
+
+
+@pytest.mark.parametrize("new,Hq", MANY)
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiles_of_falling_and_rising_scales(new, Hq, D):
+    """Whole tiles of scales from the least to the largest, in both orders, rows
+    within a tile alike or not; a first tile of zeros that takes most of the weight."""
+    for mode in ("falls", "rises", "random", "zeros"):
+        c, rows = many(new, Hq, D, len(mode))
+        n = c.table.shape[1] - 1                         # blocks of 32 keys: four to a tile
+        for j in range(n):
+            blk = c.table[:, j].long()
+            blk = blk[blk >= 0]
+            tile = j // 4
+            if mode == "zeros":
+                if tile == 0:
+                    c.vc.view(torch.uint8)[blk] = 0
+                    c.vs[blk] = 16
+                continue
+            e = {"falls": 130 - 20 * tile, "rises": 20 + 18 * tile, "random": (37 * (tile + 1)) % 115 + 18}[mode]
+            c.vs[blk] = torch.where(c.vs[blk] != 255, e, 255).to(torch.uint8)
+        if mode == "zeros":
+            u = randn(D, seed=1).float()
+            c.q = (c.q.float() * 0.5 + u).to(torch.bfloat16)
+            codes, e = Case.quantise((u * 0.4).to(torch.bfloat16)[None])
+            blk = c.table[:, 0].long()
+            c.kc[blk, :, 7], c.ks[blk, :, 7] = codes[0], e[0]
+        c.check(rows=rows)
+        c.check(window=300, rows=rows)
+
+
+@pytest.mark.parametrize("new,Hq", MANY)
+def test_scales_over_the_whole_range_many(new, Hq):
+    for lk, lv in ((90, 18), (16, 110)):
+        c, rows = many(new, Hq, 128, lk)
+        g = torch.Generator(device="cuda").manual_seed(lk)
+        for s, lo, hi in ((c.ks, lk, 121), (c.vs, lv, 135)):
+            e = torch.randint(lo, hi, s.shape, generator=g, device="cuda")
+            s.copy_(torch.where(s != 255, e, s.int()).to(torch.uint8))
+        c.check(rows=rows)
+        c.check(window=200, rows=rows)
+
+
+@pytest.mark.parametrize("T,D", [(5, 128), (68, 64), (150, 128)])
+def test_trees_over_many_sequences_of_scales_far_apart(T, D):
+    """Trees over prefixes of several tiles: the prefix's scales and the tree's."""
+    B, Hq, Hkv = 24, 8, 8
+    c = Case([500] * B, [0] * B, Hq, Hkv, D, 32, True, seed=T)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    for s, lo, hi in ((c.ks, 100, 121), (c.vs, 40, 135)):
+        e = torch.randint(lo, hi, s.shape, generator=g, device="cuda")
+        s.copy_(torch.where(s != 255, e, s.int()).to(torch.uint8))
+    h = torch.Generator().manual_seed(T)
+    q, kt, vt = randn(B, Hq, T, D, seed=1), randn(B, Hkv, T, D, seed=2), randn(B, Hkv, T, D, seed=3)
+    vt = (vt.float() * torch.pow(10.0, torch.randint(-9, 4, (B, Hkv, T, 1), generator=h).float()).cuda()).to(torch.bfloat16)
+    parent = torch.tensor([[-1 if i < 4 else i - 1 - i % 4 for i in range(T)]] * B, dtype=torch.int32).cuda()
+    ws = hta.new_q8_workspace(hta.Dims(B, Hq, Hkv, D, T, c.L_cap, 0.0))
+    out, lse = hta.verify_paged(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, workspace=ws, **c.paged())
+    assert hta.get_status(ws) == hta.OK
+    for b in (0, 11, 23):
+        i = slice(b, b + 1)
+        ref, ref_lse, absv = P.tree_rows(q[i, :2], c.kc[:, :2], c.vc[:, :2], c.table[i], c.prefix_len[i], kt[i, :2],
+                                         vt[i, :2], parent[i], c.ks[:, :2], c.vs[:, :2])
+        P.check_attention(out[i, :2], lse[i, :2], ref, ref_lse, absv)
