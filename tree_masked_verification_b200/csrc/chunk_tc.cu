@@ -64,9 +64,15 @@
 //
 // Tensor memory: S[g] columns 128g.. (fp32 scores; P as 16-bit pairs over its
 // last 64), O[g] columns 256 + gD...  P is rounded to bf16 (e4m3 caches: f16)
-// for the tensor cores, relative 2^-9 on average, the same size as the output's
-// own rounding; its sum l, the maximum and O stay in fp32.  The running maximum
-// moves only when it grew by more than 2^8 (exact after the division by l).
+// for the tensor cores, by 2^-8 of a weight at most (f16: 2^-11); its sums, the
+// maximum and O stay in fp32.  The running maximum moves only when it grew by
+// more than 2^8, so that the largest weight is a rounded one too: with bf16 O is
+// divided by the sum of what P holds, and a weight's rounding reaches the result
+// only by as much as its V differs from the result (rows with a few heavy keys,
+// scores of 8 sigma: worst row 4.1e-3 -> 2.4e-3 off, of which 2.4e-3 the output's
+// own rounding).  The lse takes the sum of the unrounded weights.  The second sum
+// costs the prefill 3 % (938 -> 966 us), ragged chunks 4-5 %, decode 2 %; made
+// behind the hand-over of P, or from weights cut off instead of rounded, the same.
 //
 // Keys a row does not see: scores are set to -inf, and rows of V that no row
 // of the item may see are zeroed in shared memory (a cache row behind the
@@ -744,7 +750,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int it_base = w.it.base, it_all_lo = w.it.all_lo, it_all_hi = w.it.all_hi, it_cache_tiles = w.it.cache_tiles;
             float m_run = -INFINITY;
             float e_run = 0.f;                              // (e4m3) O is in units of 2^(m_run + e_run - 127)
-            uint64_t l2 = 0;
+            uint64_t l2 = 0, r2 = 0;                        // sums of 2^(x - m_run); (bf16) of what P holds of them
             const int j0 = w.j0, n_tiles = w.j1 - j0;
             const int step = two ? 1 : 2;
             for (int jj = two ? 0 : grp; jj < n_tiles; jj += step) {
@@ -867,6 +873,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     if (m_tile > m_run + 8.f) {
                         const float d = m_run - m_tile, a = ex2(d);   // 0 on the first tile with a visible key
                         l2 = fma2(l2, f2(a, a), 0ull);
+                        if constexpr (!Q8) r2 = fma2(r2, f2(a, a), 0ull);
                         alpha = a;
                         resc = jj >= step;                  // (O holds nothing before the group's second tile)
                         m_run = m_tile;
@@ -906,15 +913,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     // been read by then.
                     auto weights = [&](const uint32_t (&y)[32], int q) {
                         uint32_t pk[16];
-                        uint64_t ls[2] = {0ull, 0ull};
+                        uint64_t ls[2] = {0ull, 0ull}, rs[2] = {0ull, 0ull};
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const uint64_t x2 = fma2(f2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), cc, nm);
                             const float2 z = unf2(x2), e = make_float2(ex2(z.x), ex2(z.y));
                             pk[k] = Q8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                             ls[k & 1] = add2(ls[k & 1], f2(e.x, e.y));
+                            if constexpr (!Q8) rs[k & 1] = add2(rs[k & 1], f2(bf16_lo(pk[k]), bf16_hi(pk[k])));
                         }
                         lt = add2(lt, add2(ls[0], ls[1]));
+                        if constexpr (!Q8) r2 = add2(r2, add2(rs[0], rs[1]));
                         tmem_st16(t_s + 64 + 16 * q, pk);
                     };
                     auto half_done = [&]() {
@@ -987,8 +996,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // ------------------------------------------------------ epilogue
             if (ok) ok = warp_wait(o_full, items);
             tc_fence_after();
-            const float2 lp = unf2(l2);
+            const float2 lp = unf2(l2), rp = unf2(r2);
             float l = m_run == -INFINITY ? 0.f : lp.x + lp.y, m = m_run;
+            float div = Q8 || m_run == -INFINITY ? l : rp.x + rp.y;   // what O is divided by
             float a0 = 1.f, a1 = 0.f;
             float o0 = Q8 ? ex2(e_run - 127.f) : 1.f, o1 = 1.f;      // scales of O[0], O[1] (two row tiles: of the own)
             bool has1 = false;
@@ -996,16 +1006,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 float *xch = reinterpret_cast<float *>(smem + C::OFF_XCH);
                 xch[(grp * 3 + 0) * 128 + r] = m;
                 xch[(grp * 3 + 1) * 128 + r] = row_nan || !ok ? nan : l;   // (a bad row of either group: through the sum)
-                xch[(grp * 3 + 2) * 128 + r] = o0;
+                xch[(grp * 3 + 2) * 128 + r] = Q8 ? o0 : div;
                 bar_sync(1, 256);
                 const float m0 = xch[r], m1 = xch[3 * 128 + r];
                 m = fmaxf(m0, m1);
                 a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
                 a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
                 const float l0 = xch[128 + r], l1 = xch[4 * 128 + r];
-                o0 = xch[2 * 128 + r];
-                o1 = xch[5 * 128 + r];
                 l = a0 * l0 + a1 * l1;
+                if constexpr (Q8) {
+                    o0 = xch[2 * 128 + r];
+                    o1 = xch[5 * 128 + r];
+                    div = l;
+                } else {
+                    div = a0 * xch[2 * 128 + r] + a1 * xch[5 * 128 + r];
+                }
                 row_nan = l0 != l0 || l1 != l1;
                 has1 = n_tiles > 1;
                 if constexpr (!Q8) bar_sync(1, 256);    // (rows are staged there next)
@@ -1014,7 +1029,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             const bool whole = w.j0 == 0 && w.j1 == w.it.nt;
             if (l != l) row_nan = true;
-            const float inv = row_nan ? nan : l > 0.f ? 1.f / l : 0.f;
+            const float inv = row_nan ? nan : l > 0.f ? 1.f / div : 0.f;
             const float lse = row_nan ? nan : l > 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
             const int which = w.j0 > 0 ? 0 : 1;             // the CTA's first item, begun elsewhere, or its last
             const long long prow = slot_row(p, blockIdx.x, which) + row;
