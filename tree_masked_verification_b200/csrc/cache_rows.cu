@@ -115,6 +115,9 @@ rows_kernel(const RowsParams p) {
     const bool append = p.cache.k != nullptr;
     if (append && unit == 0) check_ranges(p.q_start, p.B, p.tokens, p.status);
     if (token >= p.tokens) return;        // (whole warps)
+    // Padding: its rows need not exist, so none is read ahead of this.  (Tokens in front of
+    // q_start[B] that no sequence holds, ranges out of order, are found below.)
+    if (append && token >= p.q_start[p.B]) return;
 
     // blocks of RPW heads: q, then k, then v
     const bool has_q = p.q.p != nullptr;
@@ -141,7 +144,7 @@ rows_kernel(const RowsParams p) {
     if (append) {
         int s0 = 0, s1 = 0;
         seq = find_sequence(p.q_start, p.B, token, s0, s1);
-        if (seq < 0) return;              // padding: nothing is read or written for it
+        if (seq < 0) return;              // nothing is written for it
         const int L = p.prefix_len[seq];
         if (L < 0 || L > p.L_cap || s1 - s0 > p.L_cap - L) {
             if (lane == 0) raise_status(p.status, kStatusPrefixLenRange);
