@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the verification attention runs in
 the library's CUDA kernels.  Tensors are torch tensors on the current CUDA
 device; the library launches on torch's current stream unless a stream is
-given.  The library must have been built (``tree_masked_verification_b200.build``):
+given (what a call then allocates itself is memory of that stream; what it
+is given has to be ready there).  The library must have been built (``tree_masked_verification_b200.build``):
 there is no fallback of any kind, and a missing library raises.
 """
 from __future__ import annotations
@@ -178,6 +179,22 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _new(stream, make, *args, **kwargs):
+    """make(...): a tensor that the call allocates itself.  With a stream of
+    the caller's it is memory of that stream: filled before the kernels that
+    read it, and not handed out again before they have run.  What the call
+    returns may be used, once it is waited for, on the stream that is current
+    now."""
+    if stream is None:
+        return make(*args, **kwargs)
+    side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(side):
+        t = make(*args, **kwargs)
+    t.record_stream(here)
+    return t
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -245,11 +262,11 @@ def verify(q, k_prefix, v_prefix, prefix_len, k_tree, v_tree, parent, *, out=Non
     _need(parent, "parent", torch.int32, dev)
     dims = dims_of(q, k_prefix, scale)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        lse = _new(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = new_workspace(dims, num_splits, dev)
+        workspace = _new(stream, new_workspace, dims, num_splits, dev)
     opts = Options(int(num_splits), int(prefix_kernel),
                    prefix_events[0].cuda_event if prefix_events else None,
                    prefix_events[1].cuda_event if prefix_events else None)
@@ -274,11 +291,11 @@ def prefix_attention(q, k_prefix, v_prefix, prefix_len, *, out=None, lse=None, w
     _need(prefix_len, "prefix_len", torch.int32, dev)
     dims = dims_of(q, k_prefix, scale)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        lse = _new(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = new_workspace(dims, num_splits, dev)
+        workspace = _new(stream, new_workspace, dims, num_splits, dev)
     opts = Options(int(num_splits), int(prefix_kernel),
                    prefix_events[0].cuda_event if prefix_events else None,
                    prefix_events[1].cuda_event if prefix_events else None)
@@ -325,9 +342,9 @@ def verify_paged(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, p
     _need(parent, "parent", torch.int32, dev)
     kv = _paged(k_cache, v_cache, block_table, dev)
     dims = _paged_dims(q, k_cache, L_cap, scale)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None else lse
-    workspace = new_workspace(dims, num_splits, dev) if workspace is None else workspace
+    out = _new(stream, torch.empty_like, q) if out is None else out
+    lse = _new(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=dev) if lse is None else lse
+    workspace = _new(stream, new_workspace, dims, num_splits, dev) if workspace is None else workspace
     opts = Options(int(num_splits), PREFIX_TCGEN05,
                    prefix_events[0].cuda_event if prefix_events else None,
                    prefix_events[1].cuda_event if prefix_events else None)
@@ -352,9 +369,9 @@ def prefix_attention_paged(q, k_cache, v_cache, block_table, prefix_len, *, L_ca
     _need(prefix_len, "prefix_len", torch.int32, dev)
     kv = _paged(k_cache, v_cache, block_table, dev)
     dims = _paged_dims(q, k_cache, L_cap, scale)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None else lse
-    workspace = new_workspace(dims, num_splits, dev) if workspace is None else workspace
+    out = _new(stream, torch.empty_like, q) if out is None else out
+    lse = _new(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=dev) if lse is None else lse
+    workspace = _new(stream, new_workspace, dims, num_splits, dev) if workspace is None else workspace
     opts = Options(int(num_splits), PREFIX_TCGEN05,
                    prefix_events[0].cuda_event if prefix_events else None,
                    prefix_events[1].cuda_event if prefix_events else None)
@@ -397,9 +414,9 @@ def tree_mask(parent: torch.Tensor, workspace=None, stream=None) -> torch.Tensor
     _need(parent, "parent", torch.int32)
     B, T = parent.shape
     W = (T + 31) // 32
-    bits = torch.empty(B, T, W, dtype=torch.int32, device=parent.device)
+    bits = _new(stream, torch.empty, B, T, W, dtype=torch.int32, device=parent.device)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=parent.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=parent.device)
     _check(load().longspec_hta_tree_mask(_ptr(parent), B, T, _ptr(bits), _ptr(workspace),
                                          workspace.numel(), _stream(stream)))
     return bits
@@ -409,10 +426,10 @@ def tree_partial(q, k_tree, v_tree, parent, *, scale: float = 0.0, workspace=Non
     """Tree-only partial (debug export): (o_tree fp32 [B][Hq][T][D], lse_tree fp32)."""
     B, Hq, T, D = q.shape
     dims = Dims(B, Hq, k_tree.shape[1], D, T, 0, float(scale))
-    o = torch.empty(B, Hq, T, D, dtype=torch.float32, device=q.device)
-    l = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device)
+    o = _new(stream, torch.empty, B, Hq, T, D, dtype=torch.float32, device=q.device)
+    l = _new(stream, torch.empty, B, Hq, T, dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=q.device)
     _check(load().longspec_hta_tree_partial(ctypes.byref(dims), _ptr(q), _ptr(k_tree),
                                             _ptr(v_tree), _ptr(parent), _ptr(o), _ptr(l),
                                             _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -431,10 +448,10 @@ def prefix_partial(q, k_prefix, v_prefix, prefix_len, *, scale: float = 0.0,
     S, chunk_keys = chunking(dims, num_splits)
     S_out = ctypes.c_int(0)
     B, Hq, T, D = q.shape
-    o = torch.empty(B, Hq, T, S, D, dtype=torch.float32, device=q.device)
-    l = torch.empty(B, Hq, T, S, dtype=torch.float32, device=q.device)
+    o = _new(stream, torch.empty, B, Hq, T, S, D, dtype=torch.float32, device=q.device)
+    l = _new(stream, torch.empty, B, Hq, T, S, dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=q.device)
     _check(lib.longspec_hta_prefix_partial(ctypes.byref(dims), _ptr(q), _ptr(k_prefix),
                                            _ptr(v_prefix), _ptr(prefix_len), _ptr(o), _ptr(l),
                                            int(S), int(prefix_kernel), ctypes.byref(S_out),
@@ -471,13 +488,13 @@ def accept_greedy(logits, draft_tokens, parent, *, accept_len=None, path=None, b
     if tuple(draft_tokens.shape) != (B, T) or tuple(parent.shape) != (B, T):
         raise ValueError(f"draft_tokens/parent must be [{B}][{T}]")
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=dev)
+        accept_len = _new(stream, torch.empty, B, dtype=torch.int32, device=dev)
     if path is None:
-        path = torch.empty(B, T, dtype=torch.int32, device=dev)
+        path = _new(stream, torch.empty, B, T, dtype=torch.int32, device=dev)
     if bonus is None:
-        bonus = torch.empty(B, dtype=torch.int32, device=dev)
+        bonus = _new(stream, torch.empty, B, dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = new_accept_workspace(B, T, V, dev)
+        workspace = _new(stream, new_accept_workspace, B, T, V, dev)
     _check(load().longspec_hta_accept_greedy(
         B, T, V, _ptr(logits), _ptr(draft_tokens), _ptr(parent), _ptr(accept_len), _ptr(path),
         _ptr(bonus), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -504,11 +521,11 @@ def window_verify(q, k_ring, v_ring, prefix_len, k_tree, v_tree, parent, *, out=
     _need(parent, "parent", torch.int32, dev)
     dims = dims_of(q, k_ring, scale)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        lse = _new(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = new_window_workspace(dims, dev)
+        workspace = _new(stream, new_window_workspace, dims, dev)
     _check(load().longspec_hta_window_verify(
         ctypes.byref(dims), _ptr(q), _ptr(k_ring), _ptr(v_ring), _ptr(prefix_len), _ptr(k_tree),
         _ptr(v_tree), _ptr(parent), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
@@ -531,7 +548,7 @@ def commit(k_prefix, v_prefix, prefix_len, k_tree, v_tree, accept_len, path, *, 
         _need(t, n, torch.int32, k_tree.device)
     dims = _commit_dims(k_tree, k_prefix.shape[2])
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=k_tree.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=k_tree.device)
     _check(load().longspec_hta_commit(ctypes.byref(dims), _ptr(k_prefix), _ptr(v_prefix),
                                       _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree),
                                       _ptr(accept_len), _ptr(path), _ptr(workspace),
@@ -555,7 +572,7 @@ def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, acce
             raise ValueError(f"accept_len must be [{dims.B}]")
         st = _stream_on(dev, stream)
         if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=k_tree.device)
+            workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=k_tree.device)
         _check(load().longspec_hta_commit_paged_q8(
             dims, cache, pre, *ptrs, _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
         return
@@ -567,7 +584,7 @@ def commit_paged(k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, acce
     dims = _commit_dims(k_tree, L_cap)
     kv = _paged(k_cache, v_cache, block_table, k_tree.device)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=k_tree.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=k_tree.device)
     _check(load().longspec_hta_commit_paged(ctypes.byref(dims), ctypes.byref(kv), _ptr(prefix_len),
                                             _ptr(k_tree), _ptr(v_tree), _ptr(accept_len), _ptr(path),
                                             _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -595,6 +612,13 @@ def _stream_on(dev: int, stream) -> int:
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors are on cuda:{dev}")
     return _stream(stream)
+
+
+def _like(t, stream):
+    """A contiguous tensor of t's shape for a call's result."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=_contiguous)
+    return _new(stream, torch.empty_like, t, memory_format=_contiguous)
 
 
 def _flat(t, name, dtype, dev: int):
@@ -706,11 +730,11 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     rope = _rope(inv_freq, q_weight, k_weight, eps, interleaved, rope_scale, D, dev)
     st = _stream_on(dev, stream)
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=_contiguous)
+        q_out = _like(q, stream)
     elif q_out.shape != shape:
         raise ValueError(f"q_out must be {list(shape)}")
     if k_out is None:
-        k_out = torch.empty_like(k, memory_format=_contiguous)
+        k_out = _like(k, stream)
     elif k_out.shape != ks:
         raise ValueError(f"k_out must be {list(ks)}")
     _check((_lib or load()).longspec_hta_qk_norm_rope(
@@ -742,12 +766,12 @@ def _append(q, k, v, rope, k_cache, v_cache, block_table, prefix_len, q_start, L
     if q is not None:
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=_contiguous)
+            q_out = _like(q, stream)
         elif q_out.shape != q.shape:
             raise ValueError(f"q_out must be {list(q.shape)}")
         qh, oh = _heads(q, "q", dev, -1, 0, 1), _heads(q_out, "q_out", dev, -1, 0, 1)
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
+        workspace = _new(stream, torch.zeros, 256, dtype=torch.uint8, device=k.device)
     _check((_lib or load()).longspec_hta_append_paged(
         Dims(B, Hq, Hkv, D, N, L_cap, 0.0), qh, _heads(k, "k", dev, -1, 0, 1), _heads(v, "v", dev, -1, 0, 1), rope,
         cache, pre, start, oh, _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
@@ -818,11 +842,11 @@ def chunk_attention_paged(q, k_cache, v_cache, block_table, prefix_len, q_start,
     st = _stream_on(dev, stream)
     if Hq > 1 and q.stride(1) != D:
         raise ValueError("q: the heads of a token must be contiguous")
-    out = torch.empty_like(q, memory_format=_contiguous) if out is None else _result(out, "out", shape, _BF16, dev)
-    lse = (q.new_empty((N, Hq), dtype=torch.float32) if lse is None
+    out = _like(q, stream) if out is None else _result(out, "out", shape, _BF16, dev)
+    lse = (_new(stream, q.new_empty, (N, Hq), dtype=torch.float32) if lse is None
            else _result(lse, "lse", (N, Hq), torch.float32, dev))
     if workspace is None:
-        workspace = new_chunk_workspace(q, k_cache, B, L_cap=L_cap)
+        workspace = _new(stream, new_chunk_workspace, q, k_cache, B, L_cap=L_cap)
     _check((_lib or load()).longspec_hta_chunk_attention_paged(
         Dims(B, Hq, k_cache.shape[1], D, N, L_cap, scale), _heads(q, "q", dev, -1, 0, 1), cache, pre, start, window,
         out.data_ptr(), lse.data_ptr(), _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st))
@@ -842,10 +866,10 @@ def _attention_q8(q, k_cache, v_cache, block_table, prefix_len, tree, L_cap, out
     kt, vt, parent = tree or (None, None, None)
     _tree_shapes(dims, k_cache, prefix_len, block_table, kt, vt, parent)
     st = _stream_on(dev, stream)
-    out = torch.empty_like(q) if out is None else _result(out, "out", shape, _BF16, dev)
-    lse = (q.new_empty(shape[:3], dtype=torch.float32) if lse is None
+    out = _like(q, stream) if out is None else _result(out, "out", shape, _BF16, dev)
+    lse = (_new(stream, q.new_empty, shape[:3], dtype=torch.float32) if lse is None
            else _result(lse, "lse", shape[:3], torch.float32, dev))
-    workspace = new_q8_workspace(dims, q.device) if workspace is None else workspace
+    workspace = _new(stream, new_q8_workspace, dims, q.device) if workspace is None else workspace
     end = (out.data_ptr(), lse.data_ptr(), _flat(workspace, "workspace", torch.uint8, dev), workspace.nbytes, st)
     lib = _lib or load()
     if tree is None:
