@@ -532,7 +532,10 @@ LONGSPEC_HTA_API int longspec_hta_append_paged(const longspec_hta_dims *dims, co
  *   workspaces of their own.
  * Cache rows outside a sequence's keys, and table entries of blocks that
  * hold none of the keys its tokens see, are not read as keys (they may hold
- * anything).  Padding tokens' rows of out and lse are left as they are.
+ * anything).  An infinity or a NaN in K or V reaches the rows that see its
+ * key and no others: by its score, or in its column of the result (a row of
+ * an e4m3 cache is NaN as a whole).  Padding tokens' rows of out and lse are
+ * left as they are.
  * Errors as append; a sequence whose prefix_len is out of range gives NaN
  * rows, a table entry out of range is read as block 0 and reported. */
 LONGSPEC_HTA_API size_t longspec_hta_chunk_workspace_bytes(const longspec_hta_dims *dims);

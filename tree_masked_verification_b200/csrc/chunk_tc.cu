@@ -77,8 +77,9 @@
 // Keys a row does not see: scores are set to -inf, and rows of V that no row
 // of the item may see are zeroed in shared memory (a cache row behind the
 // last key may hold anything).  A V row that some rows see and others do not
-// is zeroed too if it holds an infinity or NaN, and the rows that see it
-// come out as NaN: 0 * inf would otherwise reach the others.
+// loses its infinities and NaN there (0 * inf would reach the others); the rows
+// that see it get them added to their columns at the end, from the cache.  (A
+// row of an e4m3 cache is NaN as a whole: zeroed, and the rows that see it NaN.)
 #include "chunk_plan.cuh"
 
 namespace hta {
@@ -117,7 +118,7 @@ struct Cfg {
     static constexpr int OFF_EXP = OFF_WALK + (Q8 ? 3 : 1) * WALK_BYTES;   // per tile in flight: E of K, E of V
     static constexpr int OFF_RED = OFF_EXP + (Q8 ? kPoisonRing * 8 : 0);   // [2][4] words: a maximum over a loader set
     static constexpr int SMEM_ALLOC = OFF_RED + (Q8 ? 32 : 0);
-    static constexpr int OFF_XCH = OFF_Q;                   // [2][3][128] floats: Q has been read by then
+    static constexpr int OFF_XCH = OFF_Q;                   // [8][128] floats: Q has been read by then
     static constexpr int OFF_PLAN = OFF_K;                  // int64 [kPlanUnits], before the first copy
     static constexpr int THREADS = Q8 ? 640 : 384;
     // registers per thread; the launch allots LAUNCH_REGS to each
@@ -207,6 +208,11 @@ __device__ __forceinline__ uint32_t max_bits(uint4 u, uint32_t big) {
     big = __vmaxu2(__vmaxu2(big, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
     return __vmaxu2(big, u.w & 0x7fff7fffu);
 }
+// eight bf16 values with infinities and NaN as 0
+__device__ __forceinline__ uint32_t finite(uint32_t x) {
+    return ((x & 0x7f80u) == 0x7f80u ? 0u : x & 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0u : x & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 finite(uint4 u) { return make_uint4(finite(u.x), finite(u.y), finite(u.z), finite(u.w)); }
 __device__ __forceinline__ uint32_t halves_max(uint32_t m) { return max(m & 0xffffu, m >> 16); }
 // eight bf16 values times `mul`, as f16
 __device__ __forceinline__ uint4 to_f16(uint4 u, float mul) {
@@ -414,10 +420,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 }
                             }
                             const bool inf = (big & 0x80008000u) != 0;
-                            if (!live || inf) {
+                            if (!live) {
 #pragma unroll
                                 for (int c = 0; c < C::HALVES * 8; ++c)
                                     *reinterpret_cast<uint4 *>(rp + (c >> 3) * C::BOX + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (inf) {
+#pragma unroll 1
+                                for (int c = 0; c < C::HALVES * 8; ++c) {
+                                    uint4 *u = reinterpret_cast<uint4 *>(rp + (c >> 3) * C::BOX + (((c & 7) ^ (r & 7)) << 4));
+                                    *u = finite(*u);
+                                }
                             }
                             word = __ballot_sync(0xffffffffu, inf);
                         }
@@ -602,8 +614,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         // tree rows (bf16), one a lane, scaled into f16 by the tile's largest value or,
                         // where the rows' largest values lie far apart, by their own (2^(127 - e);
                         // rows of zeros are zeros under any).  Rows behind the tree are zeroed, and so
-                        // are V rows with an infinity or a NaN, which are told to the softmax groups
-                        // (they wait for this tile).
+                        // are a V row's infinities and NaN, and the softmax groups told (they wait for
+                        // this tile).
                         const int r = lw * 32 + lane, live = min(128, p.N - (j - cache_tiles) * 128);
                         uint8_t *rp = stage + r * 128;
                         auto piece = [&](int x) { return reinterpret_cast<uint4 *>(rp + (x >> 3) * C::BOX + (((x & 7) ^ (r & 7)) << 4)); };
@@ -611,10 +623,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 4
                         for (int x = 0; x < D / 8; ++x) big = max_bits(*piece(x), big);
                         big = halves_max(big);
-                        const bool inf = big >= 0x7f80u, zero = r >= live || (is_v && inf);
+                        const bool inf = big >= 0x7f80u;
+                        if (inf) {                          // (the scale is that of the numbers)
+                            big = 0;
+#pragma unroll 1
+                            for (int x = 0; x < D / 8; ++x) {
+                                if (is_v) *piece(x) = finite(*piece(x));
+                                big = max_bits(finite(*piece(x)), big);
+                            }
+                            big = halves_max(big);
+                        }
                         uint32_t *red = reinterpret_cast<uint32_t *>(smem + C::OFF_RED) + (is_v ? 4 : 0);
                         const int e = 127 - f16_shift(big, 112);        // 15 .. 240
-                        const bool counts = r < live && !inf && big != 0;
+                        const bool counts = r < live && big != 0;
                         const uint32_t most = __reduce_max_sync(0xffffffffu, counts ? e : 15);
                         const uint32_t least = __reduce_min_sync(0xffffffffu, counts ? e : 255);
                         bar_sync(set_bar, 128);
@@ -629,7 +650,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         const bool each = E > lowest + spread;
                         const float mul = pow2(127 - (each ? e : E));
 #pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x) *piece(x) = zero ? make_uint4(0u, 0u, 0u, 0u) : to_f16(*piece(x), mul);
+                        for (int x = 0; x < D / 8; ++x) *piece(x) = r >= live ? make_uint4(0u, 0u, 0u, 0u) : to_f16(*piece(x), mul);
                         s_scale[at * 256 + (is_v ? 128 : 0) + r] = static_cast<uint8_t>(e);
                         if (is_v) {
                             const uint32_t nan = __ballot_sync(0xffffffffu, r < live && inf);
@@ -689,7 +710,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 qp = p.q + (w.s.s0 + t) * p.q_stride + static_cast<size_t>(h) * D;
             }
             if (w.s.bad && first_thread) raise_status(p.status, kStatusPrefixLenRange);
-            bool row_nan = w.s.bad;
+            bool row_nan = w.s.bad, row_inf = false;        // row_inf: sees a V row that lost some
             float c2_row = p.scale_log2;
             // ---- Q into shared memory (one row tile: each group half of the columns)
             {
@@ -787,7 +808,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             ok = warp_wait(v_full + (pos + jj) % C::NV, (pos + jj) / C::NV);
                             bad_v = *reinterpret_cast<const uint4 *>(s_poison + ((pos + jj) % kPoisonRing) * 4);
                         }
-                        if ((see[0] & bad_v.x) | (see[1] & bad_v.y) | (see[2] & bad_v.z) | (see[3] & bad_v.w)) row_nan = true;
+                        if ((see[0] & bad_v.x) | (see[1] & bad_v.y) | (see[2] & bad_v.z) | (see[3] & bad_v.w))
+                            (Q8 && !of_tree ? row_nan : row_inf) = true;
                         __syncwarp();
                     } else if (Q8) {
                         if (bad_v.x | bad_v.y | bad_v.z | bad_v.w) row_nan = true;
@@ -1007,6 +1029,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 xch[(grp * 3 + 0) * 128 + r] = m;
                 xch[(grp * 3 + 1) * 128 + r] = row_nan || !ok ? nan : l;   // (a bad row of either group: through the sum)
                 xch[(grp * 3 + 2) * 128 + r] = Q8 ? o0 : div;
+                xch[(6 + grp) * 128 + r] = row_inf ? 1.f : 0.f;
                 bar_sync(1, 256);
                 const float m0 = xch[r], m1 = xch[3 * 128 + r];
                 m = fmaxf(m0, m1);
@@ -1022,6 +1045,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     div = a0 * xch[2 * 128 + r] + a1 * xch[5 * 128 + r];
                 }
                 row_nan = l0 != l0 || l1 != l1;
+                row_inf = xch[6 * 128 + r] + xch[7 * 128 + r] > 0.f;
                 has1 = n_tiles > 1;
                 if constexpr (!Q8) bar_sync(1, 256);    // (rows are staged there next)
             } else if (!ok) {
@@ -1100,6 +1124,34 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             return make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
                                               __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
                         }, reinterpret_cast<uint8_t *>(p.o_part + slot_row(p, blockIdx.x, which) * D + col), D * 4);
+                }
+                if (row_inf && !row_nan && valid) {         // infinities and NaN to their columns
+                    auto add_bad = [&](const __nv_bfloat16 *v) {
+#pragma unroll 1
+                        for (int c = col0; c < col1; ++c) {
+                            const float x = __bfloat162float(v[c]);
+                            if (fabsf(x) <= 3.4e38f) continue;
+                            if (whole) p.out[orow * D + c] = __float2bfloat16(__bfloat162float(p.out[orow * D + c]) + x);
+                            else p.o_part[prow * D + c] += x;
+                        }
+                    };
+                    if constexpr (Q8) {
+                        const __nv_bfloat16 *v = p.v_tree + (static_cast<size_t>(w.cur_b) * p.Hkv + w.cur_kvh) * p.N * D;
+                        for (int node = t; node >= 0; node = s_parent[node] - 1)
+                            if (it_cache_tiles + (node >> 7) >= j0 && it_cache_tiles + (node >> 7) < w.j1)
+                                add_bad(v + static_cast<size_t>(node) * D);
+                    } else {
+                        const int32_t *table = p.cache.block_table + static_cast<size_t>(w.cur_b) * p.cache.max_blocks;
+                        for (int j = j0; j < w.j1; ++j) {
+                            if (!w.partial(j)) continue;
+                            for (int key = max(row_lo, w.key0(j)); key < min(row_hi, w.key0(j) + 128); ++key) {
+                                int n = table[key >> bsh];
+                                if (n < 0 || n >= p.cache.num_blocks) n = 0;    // (as the producers)
+                                const size_t at = (static_cast<size_t>(n) * p.Hkv + w.cur_kvh) * bs + (key & (bs - 1));
+                                add_bad(static_cast<const __nv_bfloat16 *>(p.cache.v) + at * D);
+                            }
+                        }
+                    }
                 }
                 if (valid && (two || grp == 0)) {
                     if (whole) p.lse[orow] = lse;
@@ -1195,8 +1247,8 @@ chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
                 for (int k = 0; k < DPL; ++k) acc[r][k] *= a;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    if (ls[u][r] == -INFINITY) continue;    // (a segment without visible keys, or none)
                     const float w = ex2((ls[u][r] - mn) * kLog2e);
-                    if (w == 0.f) continue;             // (a segment without visible keys, or none)
                     sum[r] += w;
 #pragma unroll
                     for (int k = 0; k < DPL; ++k) acc[r][k] = fmaf(w, v[u][r][k], acc[r][k]);
