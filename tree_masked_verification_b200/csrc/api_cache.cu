@@ -142,9 +142,19 @@ int run_attention(hta::ChunkParams &p, const longspec_hta_dims *d, const longspe
     p.g_shift = 0;
     while ((1 << p.g_shift) < p.G) ++p.g_shift;
     p.g_mul = static_cast<uint32_t>((1ull << (31 + p.g_shift)) / p.G + 1);
-    // Few rows a sequence (16 packed ones on average at most) over an e4m3
-    // cache: the kernel for few rows.
-    const bool few = q8 && !p.tree && 1LL * d->T * p.G <= 16LL * d->B;
+    // The kernel for few rows of a sequence, over an e4m3 cache.  It reads the keys
+    // once for every 8 rows (16 where chunk_decode.cu says so), against once for up to
+    // 128 or 256, and the host knows the rows on average only:
+    //   a token a sequence, up to 16 heads a KV head: 32 x 8k keys, 8 heads 60 us
+    //     against 112, 16 heads 108 against 113, one sequence of 128k 60 against 70;
+    //   up to 8 rows on average: 64 x 2 tokens of 4 heads over 4k keys 114 against
+    //     221, 63 tokens and a chunk of 40 143 against 239 (but 63 tokens of 100 keys
+    //     and a chunk of 65 at 64k 1656 against 209);
+    //   more rows gain little (12 rows: D = 128 107 against 113, D = 64 67 against 94),
+    //     and a long chunk among single tokens loses by as much as it is long (63
+    //     tokens and a chunk of 193, 4k keys: 762 against 260).  So does one chunk among
+    //     empty sequences, which T and B do not tell from single tokens.
+    const bool few = q8 && !p.tree && (d->T <= d->B ? p.G <= 16 : 1LL * d->T * p.G <= 8LL * d->B);
     const CUtensorMapSwizzle sw = !few ? CU_TENSOR_MAP_SWIZZLE_NONE
                                   : d->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     HTA_TRY(rows_map(cache->k_cache, cache_rows, d->D, cache->block_size, q8, &tm[0], sw));

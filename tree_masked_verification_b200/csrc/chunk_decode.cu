@@ -1,21 +1,21 @@
 // chunk_decode.cu -- attention of few query rows (decode steps) to a paged
-// e4m3 cache: up to 16 packed rows of a (sequence, KV head) at a time,
+// e4m3 cache, 8 or 16 packed rows of a (sequence, KV head) at a time,
 //   o = sum_j 2^{x_j} v_j / sum_j 2^{x_j},  x_j = scale * log2(e) * q.k_j.
 //
 // Bound by memory: a key's K and V are 2 (D + 1) bytes, read once, and want
 // few instructions per byte.  Tensor-core tiles of 128 rows would be mostly
-// padding here and need every code rewritten as bf16 in shared memory first
-// (chunk_tc.cu on one sequence of 256k keys: 218 us).  Here codes go from
+// padding here and need every code rewritten as f16 in shared memory first
+// (chunk_tc.cu on one sequence of 256k keys: 179 us).  Here codes go from
 // shared memory to registers and become exact f16 pairs in one conversion
 // each (e4m3 values fit f16), the operands of warp-level MMAs; the
 // row scales, powers of two, are applied to the scores and to the weights,
 // of which there are D times fewer.
 //
 // One CTA per SM takes its range of the schedule (chunk_plan.cuh, items of
-// up to 8 or 16 rows).  A producer warp keeps four or five 128-key stages of
-// codes and scale bytes on their way by TMA; four warps take the even tiles
-// and four the odd ones, 32 keys each, every warp with a running maximum, sum
-// and output of its own, joined once per item.
+// up to 8, or at D = 64 up to 16, rows).  A producer warp keeps five (D = 64:
+// eight) 128-key stages of codes and scale bytes on their way by TMA; four warps
+// take the even tiles and four the odd ones, 32 keys each, every warp with a
+// running maximum, sum and output of its own, joined once per item.
 //
 // Both products put the long side on the MMA's 16 (keys, then d) and the
 // query rows on its 8:  S^T = K Q^T,  O^T += V^T P^T.  With rows on the 16,
@@ -44,7 +44,7 @@ constexpr int kDecThreads = (kDecWarps + 1) * 32;
 template <int D, int NR>                                    // NR: groups of 8 rows
 struct DecCfg {
     static constexpr int ROWS = 8 * NR;
-    static constexpr int NS = D == 64 ? 8 : NR == 1 ? 5 : 4;   // stages
+    static constexpr int NS = D == 64 ? 8 : 5;              // stages
     static constexpr int RAW = 128 * D;
     static constexpr int STAGE = 2 * RAW + 256;             // K, V, scale bytes of K and of V
     static constexpr int OFF_STAGE = 0;                     // (codes at multiples of 1024: NS * 2 * RAW first)
@@ -517,15 +517,16 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
 
 cudaError_t launch_chunk_decode(const ChunkParams &p0, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     ChunkParams p = p0;
-    // 8 rows at a time unless sequences have more on average (a second group
-    // of 8 shares the codes' loads and conversions)
-    const bool wide = 1LL * p.N * p.G > 8LL * p.B;
+    // 8 rows at a time; at D = 64 up to 16 where a KV head has more than 8 query heads,
+    // the second group of 8 sharing the codes' loads and conversions (32 x 8k keys: 67
+    // against 93 us).  At D = 128 two groups do not fit the registers: 199 against 108.
+    const bool wide = p.D == 64 && p.G > 8;
     p.item_rows = wide ? 16 : 8;
     p.slot_rows = p.slot_rows < p.item_rows ? p.slot_rows : p.item_rows;
     p.c0 = 4;
     p.c1 = p.c2 = 4;
     p.min_share = 8;
-    if (p.D == 128) return wide ? launch<128, 2>(p, tm, stream) : launch<128, 1>(p, tm, stream);
+    if (p.D == 128) return launch<128, 1>(p, tm, stream);
     return wide ? launch<64, 2>(p, tm, stream) : launch<64, 1>(p, tm, stream);
 }
 
