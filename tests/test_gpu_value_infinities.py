@@ -59,3 +59,44 @@ def test_tree_columns_over_an_e4m3_cache(T, Hq, L, D):
     assert hta.get_status(ws) == hta.OK and torch.isfinite(lse).all()
     ref, _, absv = P.tree_rows(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, c.ks, c.vs)
     check(out, ref, absv)
+
+
+def same_or_nan(got, got_lse, ref, ref_lse, absv):
+    """Rows of a finite lse within the bound, the others NaN."""
+    ok = torch.isfinite(ref_lse)
+    assert ok.any() and not ok.all()
+    P.check_attention(got[ok], got_lse[ok], ref[ok], ref_lse[ok], absv[ok])
+    assert torch.isnan(P.cpu(got)[~ok].float()).all() and torch.isnan(P.cpu(got_lse)[~ok]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pre,new,Hq", [([200], [1], 16), ([150], [40], 4), ([130], [200], 8)])
+def test_infinite_keys(pre, new, Hq, D):
+    """A key with an infinity: weight 0 for queries whose score it makes -inf,
+    NaN for those whose score it makes +inf."""
+    c = Case(pre, new, Hq, 2, D, 16, seed=D + new[0])
+    for key in (3, pre[0] + new[0] // 2):
+        c.kc[int(c.table[0, key // 16]), :, key % 16, 7] = math.inf
+    c.q[:, ::2, 7] = -c.q[:, ::2, 7].abs() - 0.01
+    c.q[:, 1::2, 7] = c.q[:, 1::2, 7].abs() + 0.01
+    out, lse, code = c.attend()
+    assert code == hta.OK
+    ref = P.chunk_rows(c.q, c.kc, c.vc, c.table, c.prefix_len, c.q_start)
+    at = list(ref)
+    i, h = [x[0] for x in at], [x[1] for x in at]
+    same_or_nan(out[i, h], lse[i, h], torch.stack([ref[x][0] for x in at]),
+                torch.tensor([ref[x][1] for x in at], dtype=torch.float64), torch.stack([ref[x][2] for x in at]))
+
+
+@pytest.mark.parametrize("T,Hq,L,D", [(68, 4, 300, 128), (200, 4, 40, 64)])
+def test_infinite_tree_keys_over_an_e4m3_cache(T, Hq, L, D):
+    c = Case([L], [0], Hq, 2, D, 16, True, seed=T)
+    q, kt, vt = randn(1, Hq, T, D, seed=1), randn(1, 2, T, D, seed=2), randn(1, 2, T, D, seed=3)
+    q[:, :, ::2, 7] = -q[:, :, ::2, 7].abs() - 0.01
+    q[:, :, 1::2, 7] = q[:, :, 1::2, 7].abs() + 0.01
+    kt[0, :, 1, 7] = math.inf
+    kt[0, :, 8, 7] = math.inf
+    parent = torch.tensor([[-1 if i < 4 else i - 3 for i in range(T)]], dtype=torch.int32).cuda()
+    out, lse = hta.verify_paged(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, **c.paged())
+    ref, ref_lse, absv = P.tree_rows(q, c.kc, c.vc, c.table, c.prefix_len, kt, vt, parent, c.ks, c.vs)
+    same_or_nan(out, lse, ref, ref_lse, absv)
