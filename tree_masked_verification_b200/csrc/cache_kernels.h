@@ -118,6 +118,24 @@ cudaError_t launch_chunk_decode(const ChunkParams &p, const CUtensorMap (&tm)[4]
 cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_t stream);
 
+// A launch whose start may overlap the end of the kernel before it (every
+// kernel here waits for that one before it touches memory).
+struct OverlappedLaunch {
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg;
+    OverlappedLaunch(dim3 grid, dim3 block, size_t smem, cudaStream_t stream) : attr(), cfg() {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+    }
+    OverlappedLaunch(const OverlappedLaunch &) = delete;
+};
+
 // -------------------------------------------------------------- device parts
 // The sequence of token i: the largest b with q_start[b] <= i, run by a whole
 // warp as a 32-way search (two rounds for up to 1024 sequences).  Returns -1

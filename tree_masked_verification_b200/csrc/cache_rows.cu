@@ -271,19 +271,11 @@ rows_kernel(const RowsParams p) {
 
 template <int D>
 cudaError_t launch_rows_d(const RowsParams &p, unsigned grid, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kRowThreads);
-    if (!p.rotate) return cudaLaunchKernelEx(&cfg, rows_kernel<D, kRotNone>, p);
-    if (p.interleaved) return cudaLaunchKernelEx(&cfg, rows_kernel<D, kRotInterleaved>, p);
-    if (p.rot_dim == D) return cudaLaunchKernelEx(&cfg, rows_kernel<D, kRotHalves>, p);
-    return cudaLaunchKernelEx(&cfg, rows_kernel<D, kRotHalvesPartial>, p);
+    OverlappedLaunch l(dim3(grid), dim3(kRowThreads), 0, stream);
+    if (!p.rotate) return cudaLaunchKernelEx(&l.cfg, rows_kernel<D, kRotNone>, p);
+    if (p.interleaved) return cudaLaunchKernelEx(&l.cfg, rows_kernel<D, kRotInterleaved>, p);
+    if (p.rot_dim == D) return cudaLaunchKernelEx(&l.cfg, rows_kernel<D, kRotHalves>, p);
+    return cudaLaunchKernelEx(&l.cfg, rows_kernel<D, kRotHalvesPartial>, p);
 }
 
 }  // namespace
@@ -359,17 +351,9 @@ commit_q8_kernel(const CommitQ8Params p) {
 }  // namespace
 
 cudaError_t launch_commit_q8(const CommitQ8Params &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(p.B);
-    cfg.blockDim = dim3(kCommitThreads);
-    return p.D == 128 ? cudaLaunchKernelEx(&cfg, commit_q8_kernel<128>, p)
-                      : cudaLaunchKernelEx(&cfg, commit_q8_kernel<64>, p);
+    OverlappedLaunch l(dim3(p.B), dim3(kCommitThreads), 0, stream);
+    return p.D == 128 ? cudaLaunchKernelEx(&l.cfg, commit_q8_kernel<128>, p)
+                      : cudaLaunchKernelEx(&l.cfg, commit_q8_kernel<64>, p);
 }
 
 }  // namespace hta

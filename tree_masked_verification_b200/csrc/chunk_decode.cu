@@ -61,18 +61,10 @@ struct DecCfg {
     static_assert(kPlanUnits * 8 <= OFF_SCALE, "the plan's scratch lies in the stages");
 };
 
-__device__ __forceinline__ void bar_sync(int id, int n) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
 // two e4m3 codes to an f16 pair, exactly (0x7f, 0xff: NaN)
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 // d += a (16 x 16, rows) * b (16 x 8)
@@ -499,17 +491,8 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(p.grid);
-    cfg.blockDim = dim3(kDecThreads);
-    cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    e = cudaLaunchKernelEx(&cfg, chunk_decode_kernel<D, NR>, tm[0], tm[1], p);
+    OverlappedLaunch l(dim3(p.grid), dim3(kDecThreads), C::SMEM_ALLOC, stream);
+    e = cudaLaunchKernelEx(&l.cfg, chunk_decode_kernel<D, NR>, tm[0], tm[1], p);
     return e != cudaSuccess ? e : launch_chunk_merge(p, stream);
 }
 

@@ -17,6 +17,15 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, int bytes,
                  ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // bits [lo, hi) of a 32-bit word (lo, hi any integers)
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     const int h = min(max(hi, 0), 32), l = min(max(lo, 0), 32);

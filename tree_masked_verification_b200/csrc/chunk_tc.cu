@@ -138,9 +138,6 @@ struct Cfg {
 constexpr int kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpFix = 3, kWarpSoftmax = 4, kWarpLoad = 12;
 
 // ------------------------------------------------------------ small helpers
-__device__ __forceinline__ void bar_sync(int id, int n) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
 __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
     uint32_t r;
     asm volatile(
@@ -195,11 +192,6 @@ __device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w, uint32_t mult) {
         "mul.rn.f16x2 %0, a, %3;\n\t"
         "mul.rn.f16x2 %1, b, %3;\n\t}"
         : "=r"(r.x), "=r"(r.y) : "r"(w), "r"(mult));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ float pow2(int d) { return __uint_as_float(static_cast<uint32_t>(127 + d) << 23); }
@@ -1283,22 +1275,14 @@ chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.blockDim = dim3(256);
     if (p.slot_rows <= 16) {
-        cfg.gridDim = dim3(p.grid, (p.slot_rows + 7) / 8);
-        return p.D == 128 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128, 1, 8>, p)
-                          : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64, 1, 8>, p);
+        OverlappedLaunch l(dim3(p.grid, (p.slot_rows + 7) / 8), dim3(256), 0, stream);
+        return p.D == 128 ? cudaLaunchKernelEx(&l.cfg, chunk_merge_kernel<128, 1, 8>, p)
+                          : cudaLaunchKernelEx(&l.cfg, chunk_merge_kernel<64, 1, 8>, p);
     }
-    cfg.gridDim = dim3(p.grid, (p.slot_rows + 31) / 32);
-    return p.D == 128 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128, 4, 2>, p)
-                      : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64, 4, 2>, p);
+    OverlappedLaunch l(dim3(p.grid, (p.slot_rows + 31) / 32), dim3(256), 0, stream);
+    return p.D == 128 ? cudaLaunchKernelEx(&l.cfg, chunk_merge_kernel<128, 4, 2>, p)
+                      : cudaLaunchKernelEx(&l.cfg, chunk_merge_kernel<64, 4, 2>, p);
 }
 
 namespace {
@@ -1316,17 +1300,8 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) attr_set[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(p.grid);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-    e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D, Q8, ONE>, tm[0], tm[1], tm[2], tm[3], p);
+    OverlappedLaunch l(dim3(p.grid), dim3(C::THREADS), C::SMEM_ALLOC, stream);
+    e = cudaLaunchKernelEx(&l.cfg, chunk_tc_kernel<D, Q8, ONE>, tm[0], tm[1], tm[2], tm[3], p);
     if (e != cudaSuccess) return e;
     return launch_chunk_merge(p, stream);
 }
