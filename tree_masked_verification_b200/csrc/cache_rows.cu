@@ -26,7 +26,10 @@
 // row, a warp works on 4 (D = 128) or 8 (D = 64) heads of one token at a time
 // and keeps that token's cos/sin in registers; the next rows' loads are
 // issued before the current rows are computed.  Few tokens: a token's heads
-// are spread over n_split warps.
+// are spread over n_split warps.  16k tokens of 32 KV heads: bf16 88 us, 0.94 of the
+// measured copy, e4m3 68-74 us; 7 ragged chunks (4062 tokens of 32 over 8 heads)
+// normed and rotated 26 us into either cache: 0.86 of a wave of warps, each with 12
+// blocks of heads one behind the other.
 #include "cache_kernels.h"
 
 namespace hta {
@@ -94,7 +97,7 @@ __device__ __forceinline__ void store_cache_row(void *cache, uint8_t *scale, siz
 }
 
 // Four CTAs an SM (64 registers) hide more latency where they fit: rotated
-// append of ragged chunks 29.6 -> 25.4 us; interleaved pairs need 80 (a 16k
+// append of ragged chunks 29.6 -> 25.6 us; interleaved pairs need 80 (a 16k
 // chunk: 67 us with three CTAs, 78 with four).
 template <int D, int MODE>
 __global__ void __launch_bounds__(kRowThreads, MODE == kRotInterleaved ? 3 : 4)

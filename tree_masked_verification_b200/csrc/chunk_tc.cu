@@ -52,13 +52,14 @@
 // 2^-28 of the row's largest value.
 //
 // Measured (B200, 1965 MHz, at the power cap in long runs): prefill of 4096
-// tokens behind 12288, 32 heads over 8: 0.92 ms, 1.05 PFLOP/s, 0.65 of cuBLAS's
-// rate.  A pair of 128 x 128 tiles takes 3.7 k cycles against 2048 of MMA: the
-// chain of a group is its softmax (1.9 k), the MMAs of the next scores behind it
-// (1.0 k) and hand-overs, and two groups fill the MMAs to 55-60 %; issuing eight
-// MMAs takes 70 cycles, and no pipe is above 45 %.  Decode of 16 sequences, bf16:
-// 205-211 us, 0.90-0.93 of the measured copy.  A 68-node tree over e4m3 keys,
-// 8 x 32 heads: 301-310 us, 2.6 TB/s of codes: 3.0 k cycles a 128-key tile, of which
+// tokens behind 12288, 32 heads over 8: 0.96-1.00 ms, 0.96-1.00 PFLOP/s, 0.6 of
+// cuBLAS's rate.  A pair of 128 x 128 tiles took 3.7 k cycles against 2048 of MMA
+// before the second sum (below), 3.8 k by the time since: the chain of a group is
+// its softmax (1.9 k), the MMAs of the next scores behind it (1.0 k) and hand-overs,
+// and two groups fill the MMAs to 55 %; issuing eight MMAs takes 70 cycles, and no
+// pipe is above 45 %.  Decode of 16 sequences, bf16:
+// 208-213 us, 0.90-0.92 of the measured copy.  A 68-node tree over e4m3 keys,
+// 8 x 32 heads: 292-315 us, 2.6 TB/s of codes: 3.0 k cycles a 128-key tile, of which
 // the conversion's traffic in shared memory beside the MMAs' own costs 0.6 k
 // (without it 2.4 k).
 //
@@ -1311,13 +1312,16 @@ cudaError_t launch(const ChunkParams &p, const CUtensorMap (&tm)[4], cudaStream_
 cudaError_t launch_chunk_tc(const ChunkParams &p0, const CUtensorMap (&tm)[4], cudaStream_t stream) {
     ChunkParams p = p0;
     // One row tile an item where sequences have at most one on average: deeper
-    // rings for what is then bound by the keys' way to the SM.
+    // rings for what is then bound by the keys' way to the SM.  (8 chunks of 64
+    // tokens and 4 heads over 4k keys 66 us against 77 with two; 63 tokens and a chunk
+    // of 1900 219 against 238.  Over e4m3 keys the two differ less: 85 against 83,
+    // and 318 against 281.)
     const bool one = p.tree ? 1LL * p.N * p.G <= 128 : 1LL * p.N * p.G <= 128LL * p.B;
     p.item_rows = one ? 128 : 256;
     p.slot_rows = p.slot_rows < p.item_rows ? p.slot_rows : p.item_rows;
     // An item's own time (its queries' way in, its rows' way out, the pipeline's
-    // fill) is that of about two key tiles (ragged windowed chunks: 67 us with a
-    // half, 61 with two).
+    // fill) is that of about two key tiles of two row tiles, or four of one (ragged
+    // windowed chunks: 67 us with a half, 61 with two; measured there only).
     p.c0 = 18;
     p.c1 = 4;
     p.c2 = 8;
